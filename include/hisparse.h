@@ -395,6 +395,77 @@ hs_status hs_sparse_mla_decode_noalloc(const hs_layout* layout, const uint8_t* k
 /* The size of hs_sparse_mla_decode_noalloc's per-device workspace, bytes. */
 size_t hs_sparse_mla_noalloc_max_workspace(void);
 
+/*
+ * Row formats of the latent cache.  The layout's row_bytes names the format
+ * of the calls below; the resolver, the gather and the offload move rows of
+ * either as bytes.
+ *   HS_ROW_FP8  656 bytes: the rows hs_sparse_mla_decode reads -- 512 latent
+ *               values in OCP FP8 E4M3, 4 float32 scales (one per 128), 64
+ *               rope values in bfloat16.
+ *   HS_ROW_FP4  400 bytes: 512 latent values in OCP FP4 E2M1, value 2 i in
+ *               byte i's low half and 2 i + 1 in its high half; 16 E8M0 scales
+ *               (byte b: 2^(b - 127); 255: NaN), one per 32 latent values; 64
+ *               rope values in bfloat16.  A miss reads 39 % fewer bytes over
+ *               the host link than with HS_ROW_FP8.
+ * A row's latent values are its codes times their scales.
+ */
+#define HS_ROW_FP8 656
+#define HS_ROW_FP4 400
+
+/* The tokens of one hs_mla_append call.  Strides count elements. */
+typedef struct {
+  int32_t num_tokens;              /* T >= 0 */
+  int32_t num_heads;               /* H >= 0; 0: no queries to rotate */
+  const int32_t* token_req;        /* device [T]: the token's request; < 0: padding */
+  const int32_t* positions;        /* device [T]: the token's position in its request */
+  const uint16_t* latent;          /* device bf16 [T][512], 16-byte aligned */
+  int64_t latent_stride;           /* between tokens: >= 0, a multiple of 8 */
+  const uint16_t* rope;            /* device bf16 [T][64]: the keys' rope values, not rotated */
+  int64_t rope_stride;             /* between tokens: >= 0 */
+  const double* rope_freq;         /* device float64 [32]: radians a position for each pair */
+  const uint16_t* q_rope;          /* device bf16 [T][H][64], not rotated, 16-byte aligned */
+  int64_t q_token_stride;          /* >= 0, multiples of 8 */
+  int64_t q_head_stride;
+  uint16_t* q_out;                 /* device bf16 [T][H][64], 16-byte aligned; may be q_rope */
+  int64_t q_out_token_stride;      /* >= 0, multiples of 8 */
+  int64_t q_out_head_stride;
+  int32_t rope_interleaved;        /* 1: pairs (2 j, 2 j + 1); 0: pairs (j, j + 32) */
+  int32_t reserved;                /* 0 */
+} hs_append;
+
+/*
+ * hs_mla_append -- writes new tokens' rows into the paged pool, with the
+ * position rotation applied on the way, and rotates the rope part of their
+ * queries: what a forward pass does between its projections and the
+ * attention, for one layer, in one launch.
+ * Token i of request r = token_req[i] at position n = positions[i] takes row
+ *   batch->block_table[r][n / page_size] * page_size + n % page_size
+ * of layer `layer` of batch->kv_pool, in the layout's row format (HS_ROW_FP8
+ * or HS_ROW_FP4).  Its rope pairs (a, b) become (a cos - b sin, a sin + b cos)
+ * of the angles n * rope_freq[j], computed in float64 and rounded to float32,
+ * then bfloat16 (the queries' in float32 but for the angles).  A group of
+ * latent values is scaled by the smallest power of two 2^e, e >= -126, with
+ * max |x| <= 448 * 2^e (E4M3) or max |x| <= 7 * 2^e (E2M1), 1 for zeros, and
+ * rounded to nearest even, E2M1 to 6 at most; a group with a NaN or an
+ * infinity reads back as NaN.
+ * row_ids (device int32 [T], or NULL) receives the rows: -1 for padding
+ * (token_req < 0), -3 where there is none to write (a request or page beyond
+ * the table, a null placeholder, a block outside the pool).  A token with a
+ * negative row id writes nothing else, q_out and values included.
+ * values (device bf16 [T][576], 16-byte aligned, or NULL) receives the row as
+ * its readers see it: the latent values its codes stand for, then the
+ * rotated rope values.
+ * A position is written by one token of a call at most (the rows of repeated
+ * ones mix).  Uses batch->num_reqs, max_pages, block_table and kv_pool only.
+ * Errors: HS_ERR_INVALID_ARGUMENT (null or misaligned pointers with work to
+ * do, negative sizes, bad strides, a bad layer or layout),
+ * HS_ERR_UNSUPPORTED (another row_bytes, over 1,048,576 heads),
+ * HS_ERR_LAUNCH.
+ */
+hs_status hs_mla_append(const hs_layout* layout, const hs_batch* batch, int32_t layer,
+                        const hs_append* tokens, int32_t* row_ids, uint16_t* values,
+                        hipStream_t stream);
+
 /* A static English description of a status code. */
 const char* hs_status_string(hs_status status);
 

@@ -17,12 +17,15 @@ HS_MAX_ENTRIES = 8192
 HS_MAX_HOT_CAPACITY = 12288
 HS_MAX_ROW_BYTES = 4096
 HS_FILL_SYNC_WORDS = 64
+HS_ROW_FP8 = 656
+HS_ROW_FP4 = 400
 
 EXPORTS = ("hs_resolve", "hs_gather", "hs_offload_prefix_pages", "hs_plan_replay",
            "hs_resolve_grouped",
            "hs_resolve_decide", "hs_resolve_fetch", "hs_resolve_move", "hs_resolve_commit",
            "hs_page_touch", "hs_resolve_in_place", "hs_sparse_mla_decode", "hs_sparse_mla_workspace_bytes",
            "hs_sparse_mla_decode_noalloc", "hs_sparse_mla_noalloc_max_workspace",
+           "hs_mla_append",
            "hs_status_string", "hs_last_error", "hs_host_alloc", "hs_host_free",
            "hs_host_device_pointer")
 
@@ -47,6 +50,19 @@ class HsBatch(ctypes.Structure):
                 ("ctx_len", ctypes.c_void_p), ("hot_blocks", ctypes.c_void_p),
                 ("slot_token", ctypes.c_void_p), ("slot_stamp", ctypes.c_void_p),
                 ("fill_sync", ctypes.c_void_p), ("fill_sync_words", ctypes.c_int32)]
+
+
+class HsAppend(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("token_req", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("latent", ctypes.c_void_p), ("latent_stride", ctypes.c_int64),
+                ("rope", ctypes.c_void_p), ("rope_stride", ctypes.c_int64),
+                ("rope_freq", ctypes.c_void_p),
+                ("q_rope", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64),
+                ("q_out", ctypes.c_void_p), ("q_out_token_stride", ctypes.c_int64),
+                ("q_out_head_stride", ctypes.c_int64),
+                ("rope_interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -79,6 +95,7 @@ def lib():
         L.hs_sparse_mla_decode_noalloc.argtypes = [lay, vp, vp, i32, i32, vp, i32,
                                                    ctypes.c_float, vp, vp, vp]
         L.hs_sparse_mla_noalloc_max_workspace.argtypes = []
+        L.hs_mla_append.argtypes = [lay, bat, i32, ctypes.POINTER(HsAppend), vp, vp, vp]
         L.hs_status_string.argtypes = [i32]
         L.hs_status_string.restype = ctypes.c_char_p
         L.hs_last_error.argtypes = []

@@ -12,7 +12,7 @@ import ctypes
 import numpy as np
 import torch
 
-from ._lib import HS_OK, HsBatch, HsError, HsLayout, lib
+from ._lib import HS_OK, HsAppend, HsBatch, HsError, HsLayout, lib
 
 
 def _ptr(t) -> int | None:
@@ -185,6 +185,76 @@ def hs_sparse_mla_decode_noalloc(layout: HsLayout, kv_layer, row_ids, num_tokens
 
 def hs_sparse_mla_noalloc_max_workspace() -> int:
     return int(lib().hs_sparse_mla_noalloc_max_workspace())
+
+
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def _operand(t, what: str, dtypes, contiguous: bool = True):
+    """The address of an operand of the latent-cache calls: a CUDA tensor of one
+    of ``dtypes`` on the current device, an address (int), or None."""
+    if t is None or isinstance(t, int):
+        return t
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"cannot pass {type(t)} as {what}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what} is {t.dtype}, not {dtypes[0]}")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} is on {t.device}, not on the current CUDA device")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _shaped(t, what: str, shape: tuple) -> None:
+    if isinstance(t, torch.Tensor) and tuple(t.shape) != shape:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {shape}")
+
+
+def append_of(num_tokens: int, token_req, positions, latent, rope, rope_freq,
+              rope_interleaved: bool, q_rope=None, q_out=None) -> HsAppend:
+    """The tokens of one hs_mla_append call.  token_req, positions: int32 [T];
+    latent bf16 [T, 512]; rope bf16 [T, 64]; rope_freq float64 [32]; q_rope and
+    q_out (both or neither): bf16 [T, H, 64].  latent, rope, q_rope and q_out
+    may be strided views with their last dimension contiguous.  The struct keeps
+    the tensors alive."""
+    if (q_rope is None) != (q_out is None):
+        raise ValueError("q_rope and q_out go together")
+    T = num_tokens
+    heads = 0 if q_rope is None else q_rope.shape[1]
+    for t, what, shape in ((token_req, "token_req", (T,)), (positions, "positions", (T,)),
+                           (latent, "latent", (T, 512)), (rope, "rope", (T, 64)),
+                           (rope_freq, "rope_freq", (32,)), (q_rope, "q_rope", (T, heads, 64)),
+                           (q_out, "q_out", (T, heads, 64))):
+        _shaped(t, what, shape)
+    for t, what in ((latent, "latent"), (rope, "rope"), (q_rope, "q_rope"), (q_out, "q_out")):
+        if t is not None and t.stride(-1) != 1:
+            raise ValueError(f"{what}'s last dimension must be contiguous")
+    i32 = (torch.int32,)
+    a = HsAppend(T, heads, _operand(token_req, "token_req", i32),
+                 _operand(positions, "positions", i32),
+                 _operand(latent, "latent", _BF16, False), latent.stride(0),
+                 _operand(rope, "rope", _BF16, False), rope.stride(0),
+                 _operand(rope_freq, "rope_freq", (torch.float64,)),
+                 _operand(q_rope, "q_rope", _BF16, False),
+                 q_rope.stride(0) if heads else 0, q_rope.stride(1) if heads else 0,
+                 _operand(q_out, "q_out", _BF16, False),
+                 q_out.stride(0) if heads else 0, q_out.stride(1) if heads else 0,
+                 1 if rope_interleaved else 0, 0)
+    a.tensors = (token_req, positions, latent, rope, rope_freq, q_rope, q_out)
+    return a
+
+
+def hs_mla_append(layout: HsLayout, batch: HsBatch, layer: int, tokens: HsAppend, row_ids=None,
+                  values=None, stream=None) -> None:
+    """tokens: append_of(...); row_ids int32 [T] or None; values bf16 [T, 576] or
+    None."""
+    _shaped(row_ids, "row_ids", (tokens.num_tokens,))
+    _shaped(values, "values", (tokens.num_tokens, 576))
+    _check(lib().hs_mla_append(ctypes.byref(layout), ctypes.byref(batch), layer,
+                               ctypes.byref(tokens), _operand(row_ids, "row_ids", (torch.int32,)),
+                               _operand(values, "values", _BF16), _stream(stream)),
+           "hs_mla_append")
 
 
 def hs_host_alloc(nbytes: int) -> int:

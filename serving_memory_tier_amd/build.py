@@ -8,7 +8,8 @@ import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = ["resolve.hip", "copy.hip", "fetch.hip", "touch.hip", "attend.hip", "api.hip"]
+SOURCES = ["resolve.hip", "copy.hip", "fetch.hip", "touch.hip", "attend.hip", "api.hip",
+           "latent/append.hip", "latent/api.hip"]
 ARCH = "gfx950"
 
 # Packed-FP32 instructions are switched off for all HIP code (hipcc's host pass
@@ -75,11 +76,11 @@ def build(verbose: bool = False) -> str:
     build_policy()
     out = os.path.join(HERE, "libhisparse.so")
     tmp = out + ".tmp"
-    inc = ["-I", os.path.join(ROOT, "include")]
+    inc = ["-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "csrc")]
     compile_flags = [f for f in FLAGS if f != "-shared"] + ["-Rpass-analysis=kernel-resource-usage"]
     with tempfile.TemporaryDirectory(prefix="hs_build_") as objdir:
         def compile_one(src):
-            obj = os.path.join(objdir, src.replace(".hip", ".o"))
+            obj = os.path.join(objdir, src.replace("/", "_").replace(".hip", ".o"))
             return _hipcc(compile_flags + inc + ["-c", os.path.join(HERE, "csrc", src), "-o", obj],
                           src), obj
         jobs = min(len(SOURCES) + 1, max(1, os.cpu_count() or 1))

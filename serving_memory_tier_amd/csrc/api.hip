@@ -10,21 +10,23 @@
 #include <cstdio>
 
 #include "hisparse.h"
+#include "hs_check.h"
 #include "hs_internal.h"
+
+namespace hs {
 
 namespace {
 
-bool is_pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
+// The last HIP failure on this thread, for hs_last_error.
+thread_local char g_last_error[160] = "";
 
-int log2i(int64_t x) {
-  int s = 0;
-  while ((int64_t(1) << s) < x) ++s;
-  return s;
+void note(const char* what, hipError_t e) {
+  snprintf(g_last_error, sizeof g_last_error, "%s: %s (%d)", what, hipGetErrorName(e), (int)e);
 }
 
-// The kernels move 16-byte pieces: pools, outputs and layer strides are
-// 16-byte aligned.
-bool aligned16(const void* ptr) { return ((uintptr_t)ptr & 15) == 0; }
+bool is_pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
+
+}  // namespace
 
 // Checks shared by every call that reads the pool layout.
 hs_status check_layout(const hs_layout* lay) {
@@ -46,20 +48,6 @@ hs_status check_layout(const hs_layout* lay) {
   return HS_OK;
 }
 
-hs_status check_hot(const hs_layout* lay) {
-  if (lay->hot_capacity < lay->page_size || lay->hot_capacity % lay->page_size != 0)
-    return HS_ERR_INVALID_ARGUMENT;
-  if (lay->hot_capacity > HS_MAX_HOT_CAPACITY) return HS_ERR_UNSUPPORTED;
-  return HS_OK;
-}
-
-// The last HIP failure on this thread, for hs_last_error.
-thread_local char g_last_error[160] = "";
-
-void note(const char* what, hipError_t e) {
-  snprintf(g_last_error, sizeof g_last_error, "%s: %s (%d)", what, hipGetErrorName(e), (int)e);
-}
-
 hs_status from_hip(hipError_t e, const char* what) {
   if (e == hipSuccess) return HS_OK;
   note(what, e);
@@ -71,6 +59,23 @@ bool hip_ok(hipError_t e, const char* what) {
   if (e == hipSuccess) return true;
   note(what, e);
   return false;
+}
+
+}  // namespace hs
+
+namespace {
+
+using hs::aligned16;
+using hs::check_layout;
+using hs::from_hip;
+using hs::hip_ok;
+using hs::log2i;
+
+hs_status check_hot(const hs_layout* lay) {
+  if (lay->hot_capacity < lay->page_size || lay->hot_capacity % lay->page_size != 0)
+    return HS_ERR_INVALID_ARGUMENT;
+  if (lay->hot_capacity > HS_MAX_HOT_CAPACITY) return HS_ERR_UNSUPPORTED;
+  return HS_OK;
 }
 
 hs_status check_gather(const hs_layout* lay, int64_t n_rl, int64_t rows_per_rl) {
@@ -525,7 +530,7 @@ hs_status hs_sparse_mla_decode_noalloc(const hs_layout* layout, const uint8_t* k
 
 size_t hs_sparse_mla_noalloc_max_workspace(void) { return hs::kAttendScratchBytes; }
 
-const char* hs_last_error(void) { return g_last_error; }
+const char* hs_last_error(void) { return hs::g_last_error; }
 
 const char* hs_status_string(hs_status status) {
   switch (status) {
