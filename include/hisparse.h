@@ -466,6 +466,72 @@ hs_status hs_mla_append(const hs_layout* layout, const hs_batch* batch, int32_t 
                         const hs_append* tokens, int32_t* row_ids, uint16_t* values,
                         hipStream_t stream);
 
+/*
+ * hs_sparse_mla_decode_fp4 -- hs_sparse_mla_decode over 4-bit rows
+ * (layout->row_bytes must be HS_ROW_FP4, else HS_ERR_UNSUPPORTED): the same
+ * selection by row id and the same formulas, with
+ *   out bfloat16 [num_tokens][num_heads][512], lse float32; any number of
+ *   heads; q and out 16-byte aligned.
+ * Precision: keys and values are used exactly (an E2M1 value times a power of
+ * two is a bfloat16 value), scores and sums in float32, the probabilities
+ * rounded to bfloat16 for the value products, key splits merged in float32
+ * from half-precision outputs, out rounded to bfloat16.  A selected row with a
+ * NaN scale makes its token's outputs NaN.
+ * workspace: device memory of at least hs_sparse_mla_fp4_workspace_bytes(...)
+ * bytes, 16-byte aligned (may be NULL when that is 0), overwritten; calls
+ * sharing one must not overlap.
+ * Errors: HS_ERR_INVALID_ARGUMENT (null or misaligned pointers with work to
+ * do, a short workspace, num_heads < 1, negative sizes, bad layout),
+ * HS_ERR_UNSUPPORTED (another row_bytes, over 1,048,576 tokens, heads or
+ * top_k, a launch over 2^31 workgroups), HS_ERR_LAUNCH.
+ */
+hs_status hs_sparse_mla_decode_fp4(const hs_layout* layout, const uint8_t* kv_layer,
+                                   const int32_t* row_ids, int32_t num_tokens, int32_t top_k,
+                                   const uint16_t* q, int32_t num_heads, float sm_scale,
+                                   uint16_t* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace hs_sparse_mla_decode_fp4 needs for these sizes (0 when it
+ * needs none, or for non-positive sizes). */
+size_t hs_sparse_mla_fp4_workspace_bytes(int32_t num_tokens, int32_t num_heads, int32_t top_k);
+
+/*
+ * hs_paged_mla_decode -- dense latent attention through the block table, for
+ * layers without an indexer, draft layers and contexts no longer than a
+ * top-K list: every query attends to all of its request's tokens, in place.
+ * The P = num_pos query positions of request r are its P newest tokens:
+ * position p sees the tokens t <= ctx_len[r] - P + p, in layer `layer` of
+ * batch->kv_pool at row block_table[r][t / page_size] * page_size + t %
+ * page_size, FP8 or 4-bit rows by the layout's row_bytes.  Tokens without a
+ * row (a null placeholder, a block outside the pool, past the table) select
+ * nothing: out and lse are those of the tokens that are resident.
+ *   s_t = sm_scale * <q[r][p][h], key(t)>, out = sum_t softmax(s)_t value(t),
+ *   lse = log(sum_t exp(s_t)); out 0 and lse -inf where nothing is seen.
+ * A token that a position does not see has no part in its outputs, whatever
+ * its row holds; one that it sees with a NaN or an infinity makes them NaN.
+ * Arguments: q device bf16 [R][P][H][576]; out device bf16 [R][P][H][512];
+ * lse device float [R][P][H]; q and out 16-byte aligned; max_ctx: no smaller
+ * than any ctx_len[r] (tokens from max_ctx on are not attended to); the work
+ * is split by it.  Uses batch->num_reqs, max_pages, block_table, ctx_len and
+ * kv_pool.  workspace: at least hs_paged_mla_workspace_bytes(R, P, H, max_ctx)
+ * bytes, 16-byte aligned (may be NULL when that is 0), overwritten; calls
+ * sharing one must not overlap.
+ * Precision: as hs_sparse_mla_decode_fp4 (FP8 scales are applied in float32).
+ * Errors: HS_ERR_INVALID_ARGUMENT (null or misaligned pointers with work to
+ * do, a short workspace, num_pos or num_heads < 1, a negative max_ctx, a bad
+ * layer or layout), HS_ERR_UNSUPPORTED (another row_bytes, P * H over
+ * 1,048,576, a launch over 2^31 workgroups), HS_ERR_LAUNCH.
+ */
+hs_status hs_paged_mla_decode(const hs_layout* layout, const hs_batch* batch, int32_t layer,
+                              const uint16_t* q, int32_t num_pos, int32_t num_heads,
+                              int32_t max_ctx, float sm_scale, uint16_t* out, float* lse,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace hs_paged_mla_decode needs for these sizes (0 when it needs
+ * none, or for non-positive sizes). */
+size_t hs_paged_mla_workspace_bytes(int32_t num_reqs, int32_t num_pos, int32_t num_heads,
+                                    int32_t max_ctx);
+
 /* A static English description of a status code. */
 const char* hs_status_string(hs_status status);
 

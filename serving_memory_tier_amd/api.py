@@ -211,6 +211,11 @@ def _shaped(t, what: str, shape: tuple) -> None:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, not {shape}")
 
 
+def _sized(t, what: str, n: int) -> None:
+    if isinstance(t, torch.Tensor) and t.numel() != n:
+        raise ValueError(f"{what} has {t.numel()} values, not {n}")
+
+
 def append_of(num_tokens: int, token_req, positions, latent, rope, rope_freq,
               rope_interleaved: bool, q_rope=None, q_out=None) -> HsAppend:
     """The tokens of one hs_mla_append call.  token_req, positions: int32 [T];
@@ -255,6 +260,56 @@ def hs_mla_append(layout: HsLayout, batch: HsBatch, layer: int, tokens: HsAppend
                                ctypes.byref(tokens), _operand(row_ids, "row_ids", (torch.int32,)),
                                _operand(values, "values", _BF16), _stream(stream)),
            "hs_mla_append")
+
+
+def _workspace(ws) -> tuple:
+    """Address and bytes of a workspace: a contiguous CUDA tensor or None."""
+    if ws is None:
+        return None, 0
+    return _operand(ws, "workspace", (ws.dtype,)), ws.numel() * ws.element_size()
+
+
+def hs_sparse_mla_fp4_workspace_bytes(num_tokens: int, num_heads: int, top_k: int) -> int:
+    return int(lib().hs_sparse_mla_fp4_workspace_bytes(num_tokens, num_heads, top_k))
+
+
+def hs_sparse_mla_decode_fp4(layout: HsLayout, kv_layer, row_ids, num_tokens: int, top_k: int, q,
+                             num_heads: int, sm_scale: float, out, lse, workspace=None,
+                             stream=None) -> None:
+    """kv_layer: a uint8 tensor (one layer of the pool) or a device address; q bf16
+    [T, H, 576]; out bf16 [T, H, 512]; lse float32 [T, H]; workspace: a tensor of
+    hs_sparse_mla_fp4_workspace_bytes."""
+    _sized(row_ids, "row_ids", num_tokens * top_k)
+    _sized(q, "q", num_tokens * num_heads * 576)
+    _sized(out, "out", num_tokens * num_heads * 512)
+    _sized(lse, "lse", num_tokens * num_heads)
+    ws, ws_bytes = _workspace(workspace)
+    _check(lib().hs_sparse_mla_decode_fp4(
+        ctypes.byref(layout), _operand(kv_layer, "kv_layer", (torch.uint8,)),
+        _operand(row_ids, "row_ids", (torch.int32,)), num_tokens, top_k, _operand(q, "q", _BF16),
+        num_heads, sm_scale, _operand(out, "out", _BF16), _operand(lse, "lse", (torch.float32,)),
+        ws, ws_bytes, _stream(stream)), "hs_sparse_mla_decode_fp4")
+
+
+def hs_paged_mla_workspace_bytes(num_reqs: int, num_pos: int, num_heads: int, max_ctx: int) -> int:
+    return int(lib().hs_paged_mla_workspace_bytes(num_reqs, num_pos, num_heads, max_ctx))
+
+
+def hs_paged_mla_decode(layout: HsLayout, batch: HsBatch, layer: int, q, num_pos: int,
+                        num_heads: int, max_ctx: int, sm_scale: float, out, lse, workspace=None,
+                        stream=None) -> None:
+    """q bf16 [R, P, H, 576]; out bf16 [R, P, H, 512]; lse float32 [R, P, H];
+    workspace: a tensor of hs_paged_mla_workspace_bytes."""
+    rows = batch.num_reqs * num_pos * num_heads
+    _sized(q, "q", rows * 576)
+    _sized(out, "out", rows * 512)
+    _sized(lse, "lse", rows)
+    ws, ws_bytes = _workspace(workspace)
+    _check(lib().hs_paged_mla_decode(
+        ctypes.byref(layout), ctypes.byref(batch), layer, _operand(q, "q", _BF16), num_pos,
+        num_heads, max_ctx, sm_scale, _operand(out, "out", _BF16),
+        _operand(lse, "lse", (torch.float32,)), ws, ws_bytes, _stream(stream)),
+        "hs_paged_mla_decode")
 
 
 def hs_host_alloc(nbytes: int) -> int:

@@ -82,4 +82,108 @@ hs_status hs_mla_append(const hs_layout* layout, const hs_batch* batch, int32_t 
   return from_hip(hs::launch_append(p, fp4, a.rope_interleaved == 1, stream), "append launch");
 }
 
+namespace {
+
+constexpr int32_t kMaxRows = 1 << 20;   // query rows an item, tokens, list entries
+
+// Checks the workspace and the outputs of an absorbed attention call and
+// enqueues it.
+hs_status attend(hs::DecodeParams p, bool fp4, bool paged, int64_t keys, const void* out,
+                 const void* lse, void* workspace, size_t workspace_bytes, const char* what,
+                 hipStream_t stream) {
+  if (!p.q || !out || !lse || !aligned16(p.q) || !aligned16(out)) return HS_ERR_INVALID_ARGUMENT;
+  const size_t need = hs::plan_decode(p, keys);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return HS_ERR_INVALID_ARGUMENT;
+  if (!hs::decode_fits(p)) return HS_ERR_UNSUPPORTED;
+  return from_hip(hs::launch_decode(p, fp4, paged, workspace, stream), what);
+}
+
+}  // namespace
+
+hs_status hs_sparse_mla_decode_fp4(const hs_layout* layout, const uint8_t* kv_layer,
+                                   const int32_t* row_ids, int32_t num_tokens, int32_t top_k,
+                                   const uint16_t* q, int32_t num_heads, float sm_scale,
+                                   uint16_t* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream) {
+  hs_status s = check_layout(layout);
+  if (s != HS_OK) return s;
+  if (layout->row_bytes != HS_ROW_FP4) return HS_ERR_UNSUPPORTED;
+  if (num_tokens < 0 || top_k < 0 || num_heads < 1) return HS_ERR_INVALID_ARGUMENT;
+  if (num_tokens > kMaxRows || top_k > kMaxRows || num_heads > kMaxRows) return HS_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return HS_OK;
+  if (top_k > 0 && (!kv_layer || !row_ids || !aligned16(kv_layer))) return HS_ERR_INVALID_ARGUMENT;
+  hs::DecodeParams p{};
+  p.kv = kv_layer;
+  p.pool_rows = layout->pool_rows;
+  p.row_ids = row_ids;
+  p.top_k = top_k;
+  p.positions = 1;
+  p.heads = p.rows = num_heads;
+  p.items = num_tokens;
+  p.q = q;
+  p.scale = sm_scale;
+  p.out = out;
+  p.lse = lse;
+  return attend(p, true, false, top_k, out, lse, workspace, workspace_bytes,
+                "4-bit sparse MLA launch", stream);
+}
+
+size_t hs_sparse_mla_fp4_workspace_bytes(int32_t num_tokens, int32_t num_heads, int32_t top_k) {
+  if (num_tokens <= 0 || num_heads <= 0 || top_k <= 0) return 0;
+  hs::DecodeParams p{};
+  p.items = num_tokens;
+  p.rows = num_heads;
+  return hs::plan_decode(p, top_k);
+}
+
+hs_status hs_paged_mla_decode(const hs_layout* layout, const hs_batch* batch, int32_t layer,
+                              const uint16_t* q, int32_t num_pos, int32_t num_heads,
+                              int32_t max_ctx, float sm_scale, uint16_t* out, float* lse,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  hs_status s = check_layout(layout);
+  if (s != HS_OK) return s;
+  if (!batch || layer < 0 || layer >= layout->num_layers) return HS_ERR_INVALID_ARGUMENT;
+  bool fp4 = false;
+  if ((s = row_format(layout, &fp4)) != HS_OK) return s;
+  if (batch->num_reqs < 0 || batch->max_pages < 1 || num_pos < 1 || num_heads < 1 || max_ctx < 0)
+    return HS_ERR_INVALID_ARGUMENT;
+  if ((int64_t)num_pos * num_heads > kMaxRows) return HS_ERR_UNSUPPORTED;
+  if (batch->num_reqs == 0) return HS_OK;
+  if (!batch->kv_pool || !batch->block_table || !batch->ctx_len || !aligned16(batch->kv_pool))
+    return HS_ERR_INVALID_ARGUMENT;
+  hs::DecodeParams p{};
+  p.kv = batch->kv_pool + (int64_t)layer * layout->pool_layer_stride;
+  p.pool_rows = layout->pool_rows;
+  p.block_table = batch->block_table;
+  p.ctx_len = batch->ctx_len;
+  p.max_pages = batch->max_pages;
+  p.page_shift = log2i(layout->page_size);
+  const int64_t table = (int64_t)batch->max_pages << p.page_shift;
+  p.max_keys = (int32_t)(table < max_ctx ? table : max_ctx);
+  p.positions = num_pos;
+  p.heads = num_heads;
+  p.rows = num_pos * num_heads;
+  p.items = batch->num_reqs;
+  p.q = q;
+  p.scale = sm_scale;
+  p.out = out;
+  p.lse = lse;
+  // the split goes by the caller's bound, whatever the table's size: the
+  // workspace is a matter of the call's sizes alone
+  return attend(p, fp4, true, max_ctx, out, lse, workspace, workspace_bytes, "paged MLA launch",
+                stream);
+}
+
+size_t hs_paged_mla_workspace_bytes(int32_t num_reqs, int32_t num_pos, int32_t num_heads,
+                                    int32_t max_ctx) {
+  if (num_reqs <= 0 || num_pos <= 0 || num_heads <= 0 || max_ctx <= 0 ||
+      (int64_t)num_pos * num_heads > kMaxRows)
+    return 0;
+  hs::DecodeParams p{};
+  p.items = num_reqs;
+  p.rows = num_pos * num_heads;
+  return hs::plan_decode(p, max_ctx);
+}
+
 }  // extern "C"

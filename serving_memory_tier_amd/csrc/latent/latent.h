@@ -35,4 +35,39 @@ struct AppendParams {
 
 hipError_t launch_append(AppendParams p, bool fp4, bool interleaved, hipStream_t stream);
 
+// Absorbed latent attention (decode.hip): M query rows an item, 576 wide, over
+// the item's keys; 512-wide bfloat16 outputs.
+constexpr int kDecodeRows = 128;           // query rows a workgroup
+
+struct DecodeParams {
+  const uint8_t* kv;        // one layer of the pool
+  int64_t pool_rows;
+  const int32_t* row_ids;   // sparse: [items][top_k]
+  int32_t top_k;
+  const int32_t* block_table;  // paged: [items][max_pages]
+  const int32_t* ctx_len;      // paged: [items]
+  int32_t max_pages, page_shift;
+  int32_t max_keys;         // paged: keys attended to, at most (the table's, the caller's bound)
+  int32_t positions;        // paged: query positions an item
+  int32_t heads;
+  int32_t items;            // tokens, or requests
+  int32_t rows;             // M: heads, or positions * heads
+  const uint16_t* q;        // [items][rows][576]
+  float scale;
+  uint16_t* out;            // [items][rows][512]
+  float* lse;               // [items][rows]
+  // set by plan_decode and launch_decode
+  int32_t row_tiles, splits;
+  int64_t keys_per_split;   // a multiple of 32
+  uint16_t* part_o;         // [items][splits][rows][512] IEEE half, normalised
+  float* part_ml;           // [items][splits][rows][2] (maximum, sum)
+};
+
+// Sets the launch shape for items of about `keys` keys; returns the workspace's bytes.
+size_t plan_decode(DecodeParams& p, int64_t keys);
+// Whether a planned launch's grid is within the device's limits.
+bool decode_fits(const DecodeParams& p);
+hipError_t launch_decode(DecodeParams p, bool fp4, bool paged, void* workspace,
+                         hipStream_t stream);
+
 }  // namespace hs
