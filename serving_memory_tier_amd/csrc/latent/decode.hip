@@ -9,32 +9,34 @@
 //
 // Work split.  An item (a token of the sparse form, a request of the paged
 // one) has M query rows: its heads, for each of its positions.  A workgroup of
-// 8 waves takes 128 of them and one range of the item's keys.  Four wave pairs
-// take 32 rows each; a pair's waves take the two halves of the latent
-// dimensions for both products, so a wave reads only its half of a block:
+// 8 waves takes 128 of them and one range of the item's keys, in blocks of 32.
+// Four wave pairs take 32 rows each; a pair's waves take the two halves of the
+// latent dimensions for both products, so a wave reads only its half of a block:
 //   S^T (32 keys x 32 rows), 18 MFMAs 32x32x16 over 256 latent and 32 rope
 //     dimensions; the halves' sums are exchanged through LDS;
 //   the online softmax (a lane holds 16 keys of one row), in both waves alike;
 //   O^T (256 dimensions x 32 rows) += V^T P^T, 16 MFMAs; the probabilities are
 //     the B operand from registers, the values come from the row-major block
-//     through the transposing LDS read (ds_read_b64_tr_b16).
+//     through the transposing LDS reads.
 // That keeps a wave's queries (72 registers) and output (128) within 256
 // registers, two waves a SIMD, with 32 x 32 tiles: half the LDS bytes a FLOP of
 // 16-row tiles.
 //
-// Blocks of 32 rows are converted to bfloat16 once as they enter LDS, exactly:
-// E4M3 values as they are (their float32 scales, one per 128 values, multiply
-// the partial scores and the probabilities), E2M1 values times their E8M0
-// scale.  Two blocks are resident, the one after them is in registers.  Two
-// barriers a block: after the partial scores (the other buffer is free, the
-// scores are complete) and after the values (the next block is complete).
-//
-// Row strides in LDS: 1104 bytes (latent) and 144 (rope), 5 and 9 sixteen-byte
-// units modulo the banks: 16 consecutive rows' fragments fall on distinct
-// banks, and so do the transposing reads' 64-byte pieces, two deep.
+// The two row formats meet LDS in different ways:
+//   4-bit rows are converted to bfloat16 once as they enter LDS (E2M1 values
+//     times their E8M0 scale, exactly): a scale spans 32 dimensions of one
+//     key, and the transposed operand pairs keys, so scaling there would take
+//     a multiplication and a packing of every probability for each 32
+//     dimensions.  Two blocks are resident, the one after is in registers; two
+//     barriers a block.
+//   FP8 rows go from the pool into LDS as they are, with no register between
+//     (three blocks resident, one barrier a block), and are converted at each
+//     use, exactly; their float32 scales, one per 128 values, multiply the
+//     partial scores and the probabilities.  Converted copies beside the
+//     scales' accumulators would not fit the registers.
 //
 // Rounding: scores, softmax and outputs in float32; the probabilities times
-// the value scales are rounded to bfloat16 for the MFMAs (2^-8 half steps that
+// the FP8 scales are rounded to bfloat16 for the MFMAs (half steps of 2^-8 that
 // average over the keys); key splits hand over their normalised outputs in
 // half precision (2^-11), merged in float32; out is rounded to bfloat16.
 
@@ -51,12 +53,8 @@ namespace {
 constexpr int kKeys = 32;                    // rows a block
 constexpr int kLatent = 512;
 constexpr int kDim = 576;
-constexpr int kLatStride = 1072;             // bytes between latent rows in LDS
-constexpr int kRopeStride = 144;
-constexpr int kQuerySteps = 5;               // of a wave's 18 query fragments, in LDS (the rope's first)
-constexpr int kQueryRegs = 18 - kQuerySteps;
 constexpr int kSplitKeys = 2048;             // keys a split, at most: their row ids are in LDS
-constexpr int32_t kBad = -2;                 // in place of a fetched row's id: see Fetch::store
+constexpr int32_t kBad = -2;                 // in place of a fetched row's id: see Fetch4::store
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kStaleMax = 8.f;             // log2 of the largest unnormalised probability
 
@@ -69,23 +67,9 @@ typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(2))) int i32x2;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-
-struct Block {
-  uint8_t lat[kKeys * kLatStride];
-  uint8_t rope[kKeys * kRopeStride];
-  float scale[4][kKeys];                     // FP8: the rows' scales, by latent tile
-};
-
-template <int NP>
-struct Lds {
-  Block blk[2];
-  f32x4 xs[2 * NP][4][64];                   // a wave's partial scores
-  bf16x8 qs[2 * NP][kQuerySteps][64];        // a wave's queries that are not in registers
-  int32_t ids[kSplitKeys];                     // row ids, -1 where there is none
-  int32_t mine[32 * NP];                     // keys of the split that a query row sees
-  uint32_t there[kSplitKeys / 32];         // a block's keys that have one
-};
+typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
 
 // Within each 16 lanes, lane c receives element c % 4 of the 8-byte vectors at
 // the addresses of lanes 4 j + c / 4, j = 0..3.
@@ -98,9 +82,31 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
 }
 
+// Within each 16 lanes, lane c receives byte c % 8 of the 8-byte vectors at the
+// addresses of lanes 2 j + c / 8, j = 0..7.
+__device__ __forceinline__ u32x2 tr8_read(const uint8_t* p) {
+  return __builtin_bit_cast(
+      u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(const_cast<uint8_t*>(p))));
+}
+
+// Whether any of eight bfloat16 values is a NaN or an infinity.
+__device__ __forceinline__ bool bad_bf16(u32x4 w) {
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    bad |= (w[j] & 0x7f800000u) == 0x7f800000u || (w[j] & 0x7f80u) == 0x7f80u;
+  return bad;
+}
+
 template <bool HI>
 __device__ __forceinline__ uint32_t fp8_pair(uint32_t w) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
+}
+
+// Eight E4M3 bytes as bfloat16, exactly.
+__device__ __forceinline__ bf16x8 fp8x8(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(
+      bf16x8, u32x4{fp8_pair<false>(a), fp8_pair<true>(a), fp8_pair<false>(b), fp8_pair<true>(b)});
 }
 
 // The thread's number, opaque to the compiler: what it addresses with it is
@@ -111,51 +117,230 @@ __device__ __forceinline__ int fresh_tid() {
   return t;
 }
 
-// A block on its way from the pool to LDS: the latent pieces (16 bytes: 16
-// E4M3 values, or the 32 E2M1 values of one scale) in whole rounds of the
-// workgroup, then the rest of the rows (FP8: scales and rope, 9 pieces a row;
-// 4-bit: rope, 8).
-template <bool FP4, int T>
-struct Fetch {
-  static constexpr int kLat = FP4 ? 16 : 32;                   // latent pieces a row
-  static constexpr int kRest = FP4 ? 8 : 9;
-  static constexpr int kRow = FP4 ? kFp4RowBytes : kFp8RowBytes;
-  static constexpr int kRestOffset = FP4 ? 272 : 512;
+// The lists every form keeps in LDS.
+template <int NP>
+struct Lists {
+  int32_t ids[kSplitKeys];                   // row ids, -1 where there is none; kBad
+  int32_t mine[32 * NP];                     // keys of the split that a query row sees
+  uint32_t there[kSplitKeys / 32];           // a block's keys that have a row
+};
+
+// A workgroup's share: keys [lo, lo + n) of its item for query rows from row0.
+struct Share {
+  int32_t item, split, row0;
+  int64_t lo;
+  int n, edge;                               // the first query row sees the fewest keys, `edge`
+};
+
+// Finds the workgroup's share and stages its row ids; false for the grid's
+// rounding.  Ends with a barrier.
+template <bool PAGED, int NP>
+__device__ __forceinline__ bool begin(const DecodeParams& p, Lists<NP>& s, Share& sh) {
+  constexpr int T = 128 * NP;
+  // workgroup -> (item, split, row tile): the row tiles of one (item, split)
+  // are 8 workgroups apart, the XCD stride, so one's rows are in the other's L2
+  const int64_t L = blockIdx.x;
+  const int tile = (int)((L >> 3) % p.row_tiles);
+  const int64_t pair = L / (8 * p.row_tiles) * 8 + (L & 7);
+  if (pair >= (int64_t)p.items * p.splits) return false;
+  sh.item = (int32_t)(pair % p.items);
+  sh.split = (int32_t)(pair / p.items);
+  sh.row0 = tile * 32 * NP;
+  sh.lo = (int64_t)sh.split * p.keys_per_split;
+  const int tid = threadIdx.x, l = tid & 63;
+  const int32_t rows = min(32 * NP, p.rows - sh.row0);
+  int64_t keys, unseen;                      // a query row sees unseen + its position of the keys
+  if constexpr (PAGED) {
+    const int64_t ctx = max(p.ctx_len[sh.item], 0);
+    keys = min(ctx, (int64_t)p.max_keys);
+    unseen = ctx - p.positions + 1;
+  } else {
+    keys = unseen = p.top_k;
+  }
+  auto seen = [&](int32_t row) {
+    return (int)max((int64_t)0, min(p.keys_per_split,
+                                    min(keys, unseen + (sh.row0 + row) / p.heads) - sh.lo));
+  };
+  sh.n = seen(rows - 1);
+  sh.edge = seen(0);
+  if (tid < 32 * NP) s.mine[tid] = seen(min(tid, rows - 1));
+  for (int k = tid; k < (sh.n + 63) / 64 * 64; k += T) {
+    int32_t id = -1;
+    if (k < sh.n) {
+      if constexpr (PAGED) {
+        const int64_t t = sh.lo + k;
+        const int32_t b = p.block_table[(int64_t)sh.item * p.max_pages + (t >> p.page_shift)];
+        if (b >= 0 && b < p.pool_rows >> p.page_shift)
+          id = (b << p.page_shift) | (int32_t)(t & ((1 << p.page_shift) - 1));
+      } else {
+        id = p.row_ids[(int64_t)sh.item * p.top_k + sh.lo + k];
+        if (id >= p.pool_rows) id = -1;
+      }
+    }
+    s.ids[k] = id;
+    const uint64_t b = __ballot(id >= 0);
+    if (l == 0) s.there[k >> 5] = (uint32_t)b;
+    if (l == 32) s.there[k >> 5] = (uint32_t)(b >> 32);
+  }
+  __syncthreads();
+  return true;
+}
+
+// Thread t's query row of the item, or -1 past the last.
+template <int NP>
+__device__ __forceinline__ int32_t query_row(const DecodeParams& p, const Share& sh, int t) {
+  const int32_t m = sh.row0 + (t >> 6) % NP * 32 + (t & 31);
+  return m < p.rows ? m : -1;
+}
+
+// Masks a block's scores (keys without a row, and keys the row does not see)
+// where it has any to mask.
+template <bool PAGED, int NP>
+__device__ __forceinline__ void mask(const Lists<NP>& s, const Share& sh, int bi, int row, int hi,
+                                     f32x16& sc) {
+  const uint32_t there = s.there[bi];
+  if (there == 0xffffffffu && (bi + 1) * kKeys <= sh.edge) return;
+  const int left = s.mine[row] - bi * kKeys;
+  uint32_t seen = left >= kKeys ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
+  seen = (seen & there) >> (4 * hi);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {             // key 8 (i / 4) + 4 hi + i % 4
+    if (PAGED && s.ids[bi * kKeys + 4 * hi + 8 * (i / 4) + i % 4] == kBad)
+      sc[i] = __builtin_nanf("");
+    if (!(seen & (1u << (8 * (i / 4) + i % 4)))) sc[i] = -INFINITY;
+  }
+}
+
+// One block of the online softmax: scores (in log2 units) to probabilities.
+// The maximum is renewed, and the output rescaled, only when it grows by 2^8.
+__device__ __forceinline__ void softmax(f32x16& sc, float& m_run, float& l_run, f32x16 (&o)[8]) {
+  float mb = sc[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) mb = fmaxf(mb, sc[i]);
+  mb = fmaxf(mb, __shfl_xor(mb, 32));
+  const bool grow = mb > m_run + kStaleMax;
+  const float m_new = grow ? mb : m_run;
+  const float alpha = grow ? __builtin_amdgcn_exp2f(m_run - m_new) : 1.f;
+  const float base = m_new == -INFINITY ? 0.f : m_new;    // nothing seen yet: exp2(-inf) = 0
+  float ls = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    sc[i] = __builtin_amdgcn_exp2f(sc[i] - base);
+    ls += sc[i];
+  }
+  l_run = l_run * alpha + ls;
+  m_run = m_new;
+  if (__any(grow)) {
+#pragma unroll
+    for (int dt = 0; dt < 8; ++dt) o[dt] *= alpha;
+  }
+}
+
+// Writes this lane's 128 output values and, once a row, its log sum: the
+// result, or the split's share of it.
+template <int NP>
+__device__ __forceinline__ void finish(const DecodeParams& p, const Share& sh, const f32x16 (&o)[8],
+                                       float m_run, float l_run) {
+  const int tid = fresh_tid(), hi = (tid & 63) >> 5, half = (tid >> 6) / NP;
+  const int32_t m = query_row<NP>(p, sh, tid);
+  if (m < 0) return;
+  l_run += __shfl_xor(l_run, 32);              // the same query row
+  const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+  const int d0 = half * 256 + 4 * hi;
+  const int64_t mrow = (int64_t)sh.item * p.rows + m;
+  if (p.splits == 1) {
+    uint16_t* out = p.out + mrow * kLatent + d0;
+#pragma unroll
+    for (int dt = 0; dt < 8; ++dt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<u32x2*>(out + 32 * dt + 8 * i) =
+            u32x2{bf16_pair(o[dt][4 * i] * inv, o[dt][4 * i + 1] * inv),
+                  bf16_pair(o[dt][4 * i + 2] * inv, o[dt][4 * i + 3] * inv)};
+    if (half == 0 && hi == 0)
+      p.lse[mrow] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) / kLog2e;
+    return;
+  }
+  const int64_t ps = ((int64_t)sh.item * p.splits + sh.split) * p.rows + m;
+  if (half == 0 && hi == 0) {
+    p.part_ml[2 * ps] = m_run;
+    p.part_ml[2 * ps + 1] = l_run;
+  }
+  if (l_run == 0.f) return;                    // the merge does not read it
+  uint16_t* po = p.part_o + ps * kLatent + d0;
+#pragma unroll
+  for (int dt = 0; dt < 8; ++dt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<f16x4*>(po + 32 * dt + 8 * i) =
+          f16x4{(_Float16)(o[dt][4 * i] * inv), (_Float16)(o[dt][4 * i + 1] * inv),
+                (_Float16)(o[dt][4 * i + 2] * inv), (_Float16)(o[dt][4 * i + 3] * inv)};
+}
+
+// ------------------------------------------------------------ 4-bit rows
+
+// Row strides in LDS: 1072 bytes (latent) and 144 (rope), 3 and 9 sixteen-byte
+// units modulo the banks: 16 consecutive rows' fragments fall on distinct
+// banks, and the rows of a transposing read do not overlap.
+constexpr int kLatStride = 1072;
+constexpr int kRopeStride = 144;
+// Of a wave's 18 query fragments, the last are kept in LDS.
+constexpr int kQuerySteps = 5;
+constexpr int kQueryRegs = 18 - kQuerySteps;
+
+struct Block4 {
+  uint8_t lat[kKeys * kLatStride];
+  uint8_t rope[kKeys * kRopeStride];
+};
+
+template <int NP>
+struct Lds4 {
+  Block4 blk[2];
+  f32x4 xs[2 * NP][4][64];                   // a wave's partial scores
+  bf16x8 qs[2 * NP][kQuerySteps][64];
+  Lists<NP> lists;
+};
+
+// A block on its way from the pool to LDS: 16 latent pieces a row (16 bytes,
+// the 32 values of one scale), then its 8 rope pieces.
+template <int T>
+struct Fetch4 {
+  static constexpr int kLat = 16, kRope = 8;
   static constexpr int kLatRounds = kKeys * kLat / T;
-  static constexpr int kRestRounds = (kKeys * kRest + T - 1) / T;
+  static constexpr int kRopeRounds = (kKeys * kRope + T - 1) / T;
   static_assert(kKeys * kLat % T == 0, "whole rounds");
 
   u32x4 lat[kLatRounds];
-  u32x4 rest[kRestRounds];
-  uint32_t scale[FP4 ? kLatRounds : 1];
+  u32x4 rope[kRopeRounds];
+  uint32_t scale[kLatRounds];
   uint32_t there;                                              // bit a piece: its row is there
 
   __device__ __forceinline__ void load(const uint8_t* kv, const int32_t* ids) {
     const int tid = fresh_tid();
-    int32_t id[kLatRounds + kRestRounds];
+    int32_t id[kLatRounds + kRopeRounds];
 #pragma unroll
     for (int i = 0; i < kLatRounds; ++i) id[i] = ids[(tid + T * i) / kLat];
 #pragma unroll
-    for (int i = 0; i < kRestRounds; ++i) {
+    for (int i = 0; i < kRopeRounds; ++i) {
       const int q = tid + T * i;
-      id[kLatRounds + i] = q < kKeys * kRest ? ids[q / kRest] : -1;
+      id[kLatRounds + i] = q < kKeys * kRope ? ids[q / kRope] : -1;
     }
     there = 0;
 #pragma unroll
     for (int i = 0; i < kLatRounds; ++i) {
       // a key without a row reads row 0 and is stored as zeros
-      const uint8_t* row = kv + (int64_t)max(id[i], 0) * kRow;
+      const uint8_t* row = kv + (int64_t)max(id[i], 0) * kFp4RowBytes;
       const int pc = (tid + T * i) % kLat;
       lat[i] = *reinterpret_cast<const u32x4*>(row + 16 * pc);
-      if constexpr (FP4) scale[i] = row[256 + pc];
+      scale[i] = row[256 + pc];
       there |= (id[i] >= 0 ? 1u : 0u) << i;
     }
 #pragma unroll
-    for (int i = 0; i < kRestRounds; ++i) {
+    for (int i = 0; i < kRopeRounds; ++i) {
       const int q = tid + T * i;
-      const uint8_t* row = kv + (int64_t)max(id[kLatRounds + i], 0) * kRow;
-      if (q < kKeys * kRest)
-        rest[i] = *reinterpret_cast<const u32x4*>(row + kRestOffset + 16 * (q % kRest));
+      const uint8_t* row = kv + (int64_t)max(id[kLatRounds + i], 0) * kFp4RowBytes;
+      if (q < kKeys * kRope)
+        rope[i] = *reinterpret_cast<const u32x4*>(row + 272 + 16 * (q % kRope));
       there |= (id[kLatRounds + i] >= 0 ? 1u : 0u) << (kLatRounds + i);
     }
   }
@@ -164,120 +349,56 @@ struct Fetch {
   // others, where a probability of 0 times a NaN or an infinity would be NaN:
   // pieces that hold one are stored as zeros and their row's id, no longer
   // needed, becomes kBad: its scores are NaN for the query rows that see it.
-  __device__ __forceinline__ void store(Block& b, int32_t* ids, bool sanitize, int from) {
+  __device__ __forceinline__ void store(Block4& b, int32_t* ids, bool sanitize, int from) {
     const int tid = fresh_tid();
 #pragma unroll
     for (int i = 0; i < kLatRounds; ++i) {
       const int q = tid + T * i, k = q / kLat, pc = q % kLat;
       u32x4 w = (there >> i) & 1 ? lat[i] : u32x4{0u, 0u, 0u, 0u};
-      uint8_t* dst = b.lat + k * kLatStride + pc * (FP4 ? 64 : 32);
-      if constexpr (FP4) {
-        uint32_t sb = (there >> i) & 1 ? scale[i] : 127u;
-        if (sanitize && k >= from && sb == 255u) {
-          ids[k] = kBad;
-          w = u32x4{0u, 0u, 0u, 0u};
-          sb = 127u;
-        }
-        const float s = __builtin_bit_cast(float, sb << 23);   // 255: infinity, whose product is NaN
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const u32x4 v = {
-              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 0)),
-              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 1)),
-              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 2)),
-              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 3))};
-          *reinterpret_cast<u32x4*>(dst + 16 * j) = v;
-        }
-      } else {
-        if (sanitize && k >= from) {
-          bool nan = false;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) nan |= ((w[j / 4] >> (8 * (j % 4))) & 0x7fu) == 0x7fu;
-          if (nan) {
-            ids[k] = kBad;
-            w = u32x4{0u, 0u, 0u, 0u};
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          *reinterpret_cast<u32x4*>(dst + 16 * j) =
-              u32x4{fp8_pair<false>(w[2 * j]), fp8_pair<true>(w[2 * j]),
-                    fp8_pair<false>(w[2 * j + 1]), fp8_pair<true>(w[2 * j + 1])};
+      uint32_t sb = (there >> i) & 1 ? scale[i] : 127u;
+      if (sanitize && k >= from && sb == 255u) {
+        ids[k] = kBad;
+        w = u32x4{0u, 0u, 0u, 0u};
+        sb = 127u;
       }
+      const float s = __builtin_bit_cast(float, sb << 23);     // 255: infinity, whose product is NaN
+      uint8_t* dst = b.lat + k * kLatStride + 64 * pc;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<u32x4*>(dst + 16 * j) = u32x4{
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 0)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 1)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 2)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 3))};
     }
 #pragma unroll
-    for (int i = 0; i < kRestRounds; ++i) {
+    for (int i = 0; i < kRopeRounds; ++i) {
       const int q = tid + T * i;
-      if (q >= kKeys * kRest) continue;
-      const int k = q / kRest, pc = q % kRest;
-      u32x4 w = (there >> (kLatRounds + i)) & 1 ? rest[i] : u32x4{0u, 0u, 0u, 0u};
-      const bool scales = !FP4 && pc == 0;
-      if (sanitize && k >= from) {
-        bool nan = false;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          nan |= (w[j] & 0x7f800000u) == 0x7f800000u ||
-                 (!scales && (w[j] & 0x7f80u) == 0x7f80u);
-        if (nan) {
-          ids[k] = kBad;
-          w = u32x4{0u, 0u, 0u, 0u};
-        }
+      if (q >= kKeys * kRope) continue;
+      const int k = q / kRope;
+      u32x4 w = (there >> (kLatRounds + i)) & 1 ? rope[i] : u32x4{0u, 0u, 0u, 0u};
+      if (sanitize && k >= from && bad_bf16(w)) {
+        ids[k] = kBad;
+        w = u32x4{0u, 0u, 0u, 0u};
       }
-      if (scales) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) b.scale[t][k] = __builtin_bit_cast(float, w[t]);
-      } else {
-        *reinterpret_cast<u32x4*>(b.rope + k * kRopeStride + 16 * (FP4 ? pc : pc - 1)) = w;
-      }
+      *reinterpret_cast<u32x4*>(b.rope + k * kRopeStride + 16 * (q % kRope)) = w;
     }
   }
 };
 
-template <bool FP4, bool PAGED, int NP>
-__global__ void __launch_bounds__(128 * NP) decode_kernel(DecodeParams p) {
+template <bool PAGED, int NP>
+__global__ void __launch_bounds__(128 * NP) decode_fp4_kernel(DecodeParams p) {
   constexpr int T = 128 * NP;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
-  Lds<NP>& s = *reinterpret_cast<Lds<NP>*>(lds_raw);
-  // workgroup -> (item, split, row tile): the row tiles of one (item, split)
-  // are 8 workgroups apart, the XCD stride, so one's rows are in the other's L2
-  const int64_t L = blockIdx.x;
-  const int tile = (int)((L >> 3) % p.row_tiles);
-  const int64_t pair = L / (8 * p.row_tiles) * 8 + (L & 7);
-  if (pair >= (int64_t)p.items * p.splits) return;     // the grid's rounding: the whole workgroup
-  const int32_t item = (int32_t)(pair % p.items), split = (int32_t)(pair / p.items);
-  const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, hi = l >> 5, half = w / NP;
-  const int32_t row0 = tile * 32 * NP;
-  // the keys of this workgroup: [lo, lo + n); the first query row sees the
-  // fewest of them, `edge`
-  const int64_t lo = (int64_t)split * p.keys_per_split;
-  int n, edge;
-  {
-    const int64_t most = p.keys_per_split;
-    const int32_t rows = min(32 * NP, p.rows - row0);
-    int64_t keys, unseen;                      // a query row sees unseen + its position of the keys
-    if constexpr (PAGED) {
-      const int64_t ctx = max(p.ctx_len[item], 0);
-      keys = min(ctx, (int64_t)p.max_keys);
-      unseen = ctx - p.positions + 1;
-    } else {
-      keys = unseen = p.top_k;
-    }
-    auto seen = [&](int32_t row) {
-      return (int)max((int64_t)0, min(most, min(keys, unseen + (row0 + row) / p.heads) - lo));
-    };
-    n = seen(rows - 1);
-    edge = seen(0);
-    if (tid < 32 * NP) s.mine[tid] = seen(min(tid, rows - 1));
-  }
-
-  // a lane past the last row takes row 0's queries; it writes nothing
-  auto query_row = [&](int t) {
-    const int32_t m = row0 + (t >> 6) % NP * 32 + (t & 31);
-    return m < p.rows ? m : -1;
-  };
+  Lds4<NP>& s = *reinterpret_cast<Lds4<NP>*>(lds_raw);
+  Share sh;
+  if (!begin<PAGED, NP>(p, s.lists, sh)) return;       // the whole workgroup
   bf16x8 qb[kQueryRegs];
   {
-    const uint16_t* q = p.q + ((int64_t)item * p.rows + max(query_row(tid), 0)) * kDim;
+    // a lane past the last row takes row 0's queries; it writes nothing
+    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, hi = l >> 5, half = w / NP;
+    const uint16_t* q =
+        p.q + ((int64_t)sh.item * p.rows + max(query_row<NP>(p, sh, tid), 0)) * kDim;
 #pragma unroll
     for (int ks = 0; ks < 18; ++ks) {
       const int at = ks < 16 ? half * 256 + ks * 16 + 8 * hi
@@ -296,36 +417,17 @@ __global__ void __launch_bounds__(128 * NP) decode_kernel(DecodeParams p) {
     for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
   float m_run = -INFINITY, l_run = 0.f;        // l_run: this lane's keys only
   const float qk_scale = p.scale * kLog2e;
-
-  const int blocks = (n + kKeys - 1) / kKeys;
-  for (int k = tid; k < (n + 63) / 64 * 64; k += T) {
-    int32_t id = -1;
-    if (k < n) {
-      if constexpr (PAGED) {
-        const int64_t t = lo + k;
-        const int32_t b = p.block_table[(int64_t)item * p.max_pages + (t >> p.page_shift)];
-        if (b >= 0 && b < p.pool_rows >> p.page_shift)
-          id = (b << p.page_shift) | (int32_t)(t & ((1 << p.page_shift) - 1));
-      } else {
-        id = p.row_ids[(int64_t)item * p.top_k + lo + k];
-        if (id >= p.pool_rows) id = -1;
-      }
-    }
-    s.ids[k] = id;
-    const uint64_t b = __ballot(id >= 0);
-    if (l == 0) s.there[k >> 5] = (uint32_t)b;
-    if (l == 32) s.there[k >> 5] = (uint32_t)(b >> 32);
-  }
-  __syncthreads();
-  Fetch<FP4, T> f;
+  int32_t* ids = s.lists.ids;
+  const int blocks = (sh.n + kKeys - 1) / kKeys;
+  Fetch4<T> f;
   if (blocks > 0) {
-    f.load(p.kv, s.ids);
-    f.store(s.blk[0], s.ids, PAGED && kKeys > edge, edge);
-    if (blocks > 1) f.load(p.kv, s.ids + kKeys);
+    f.load(p.kv, ids);
+    f.store(s.blk[0], ids, PAGED && kKeys > sh.edge, sh.edge);
+    if (blocks > 1) f.load(p.kv, ids + kKeys);
   }
   __syncthreads();
   for (int bi = 0; bi < blocks; ++bi) {
-    Block& cb = s.blk[bi & 1];
+    const Block4& cb = s.blk[bi & 1];
     const int tid = fresh_tid(), w = tid >> 6, l = tid & 63;
     const int col = l & 31, hi = l >> 5, duo = w % NP, half = w / NP;
     auto query = [&](int ks) { return ks < kQueryRegs ? qb[ks] : s.qs[w][ks - kQueryRegs][l]; };
@@ -335,34 +437,11 @@ __global__ void __launch_bounds__(128 * NP) decode_kernel(DecodeParams p) {
     for (int i = 0; i < 16; ++i) sc[i] = 0.f;
     const uint8_t* krow = cb.lat + col * kLatStride + half * 512 + 16 * hi;
     const uint8_t* rrow = cb.rope + col * kRopeStride + half * 64 + 16 * hi;
-    if constexpr (FP4) {
 #pragma unroll
-      for (int ks = 0; ks < 16; ++ks)
-        sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            *reinterpret_cast<const bf16x8*>(krow + 32 * ks), query(ks), sc, 0, 0, 0);
-    } else {
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        f32x16 acc;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              *reinterpret_cast<const bf16x8*>(krow + 32 * (8 * t + ks)), query(8 * t + ks),
-              acc, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f32x4 k4 = *reinterpret_cast<const f32x4*>(&cb.scale[2 * half + t][8 * i + 4 * hi]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sc[4 * i + j] += k4[j] * acc[4 * i + j];
-        }
-      }
-    }
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
+    for (int ks = 0; ks < 18; ++ks)
       sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-          *reinterpret_cast<const bf16x8*>(rrow + 32 * ks), query(16 + ks), sc, 0, 0, 0);
+          *reinterpret_cast<const bf16x8*>(ks < 16 ? krow + 32 * ks : rrow + 32 * (ks - 16)),
+          query(ks), sc, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       s.xs[w][i][l] = f32x4{sc[4 * i], sc[4 * i + 1], sc[4 * i + 2], sc[4 * i + 3]};
@@ -376,119 +455,242 @@ __global__ void __launch_bounds__(128 * NP) decode_kernel(DecodeParams p) {
       for (int j = 0; j < 4; ++j) sc[4 * i + j] = (sc[4 * i + j] + v[j]) * qk_scale;
     }
     if (bi + 1 < blocks) {
-      f.store(s.blk[(bi + 1) & 1], s.ids + (bi + 1) * kKeys, PAGED && (bi + 2) * kKeys > edge, edge - (bi + 1) * kKeys);
-      if (bi + 2 < blocks) f.load(p.kv, s.ids + (bi + 2) * kKeys);
+      f.store(s.blk[(bi + 1) & 1], ids + (bi + 1) * kKeys, PAGED && (bi + 2) * kKeys > sh.edge,
+              sh.edge - (bi + 1) * kKeys);
+      if (bi + 2 < blocks) f.load(p.kv, ids + (bi + 2) * kKeys);
     }
-    // ---- masks: keys without a row, and keys this row does not see
-    const uint32_t there = s.there[bi];
-    if (there != 0xffffffffu || (bi + 1) * kKeys > edge) {
-      const int left = s.mine[duo * 32 + col] - bi * kKeys;
-      uint32_t seen = left >= kKeys ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
-      seen = (seen & there) >> (4 * hi);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {           // key 8 (i / 4) + 4 hi + i % 4
-        if (PAGED && s.ids[bi * kKeys + 4 * hi + 8 * (i / 4) + i % 4] == kBad)
-          sc[i] = __builtin_nanf("");
-        if (!(seen & (1u << (8 * (i / 4) + i % 4)))) sc[i] = -INFINITY;
-      }
-    }
-    // ---- online softmax; the maximum is renewed only when it grows by 2^8
-    float mb = sc[0];
-#pragma unroll
-    for (int i = 1; i < 16; ++i) mb = fmaxf(mb, sc[i]);
-    mb = fmaxf(mb, __shfl_xor(mb, 32));
-    const bool grow = mb > m_run + kStaleMax;
-    const float m_new = grow ? mb : m_run;
-    const float alpha = grow ? __builtin_amdgcn_exp2f(m_run - m_new) : 1.f;
-    const float base = m_new == -INFINITY ? 0.f : m_new;    // nothing seen yet: exp2(-inf) = 0
-    float pr[16], ls = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      pr[i] = __builtin_amdgcn_exp2f(sc[i] - base);
-      ls += pr[i];
-    }
-    l_run = l_run * alpha + ls;
-    m_run = m_new;
-    if (__any(grow)) {
-#pragma unroll
-      for (int dt = 0; dt < 8; ++dt) o[dt] *= alpha;
-    }
+    mask<PAGED, NP>(s.lists, sh, bi, duo * 32 + col, hi, sc);
+    softmax(sc, m_run, l_run, o);
     // ---- O^T += V^T P^T.  Step ks covers keys 16 ks + 4 hi + {0..3, 8..11},
     // the ones this lane holds; lane c of a 16-lane group supplies row c / 4
     // and 4 dimensions of each transposing read
     const uint8_t* vrow = cb.lat + (4 * hi + ((l & 15) >> 2)) * kLatStride + half * 512 +
                           32 * ((l >> 4) & 1) + 8 * (l & 3);
+    bf16x8 pb[2];
 #pragma unroll
-    for (int t = 0; t < (FP4 ? 1 : 2); ++t) {
+    for (int ks = 0; ks < 2; ++ks)
+      pb[ks] = __builtin_bit_cast(
+          bf16x8, u32x4{bf16_pair(sc[8 * ks], sc[8 * ks + 1]), bf16_pair(sc[8 * ks + 2], sc[8 * ks + 3]),
+                        bf16_pair(sc[8 * ks + 4], sc[8 * ks + 5]),
+                        bf16_pair(sc[8 * ks + 6], sc[8 * ks + 7])});
+#pragma unroll
+    for (int dt = 0; dt < 8; ++dt)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const u32x2 a = tr16_read(vrow + 16 * ks * kLatStride + 64 * dt);
+        const u32x2 b = tr16_read(vrow + (16 * ks + 8) * kLatStride + 64 * dt);
+        o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]}), pb[ks], o[dt], 0, 0, 0);
+      }
+    __syncthreads();
+  }
+  finish<NP>(p, sh, o, m_run, l_run);
+}
+
+// -------------------------------------------------------------- FP8 rows
+
+constexpr int kPieces = kFp8RowBytes / 16;   // 41
+constexpr int kScales = 512, kRope = 528;    // offsets in a row
+
+constexpr int kQuerySteps8 = 7;              // query fragments in LDS, the last
+
+// Rows lie in LDS as in the pool, 656 bytes apart (an odd number of 16-byte
+// units: rows' fragments on distinct banks).
+template <int NP>
+struct Lds8 {
+  uint8_t blk[3][kKeys * kFp8RowBytes];
+  f32x4 xs[2 * NP][4][64];                   // a wave's partial scores
+  bf16x8 qs[2 * NP][kQuerySteps8][64];
+  Lists<NP> lists;
+};
+
+// What a key without a row reads.
+__device__ __attribute__((aligned(16))) uint8_t zero_row[kFp8RowBytes];
+
+// A block's rows from the pool straight into LDS, 16 bytes a lane; wait_rows()
+// and a barrier before they are read.
+template <int T>
+__device__ __forceinline__ void fetch_rows(const uint8_t* kv, const int32_t* ids, uint8_t* blk) {
+  const int tid = fresh_tid(), first = __builtin_amdgcn_readfirstlane(tid);
+#pragma unroll
+  for (int i = 0; i < (kKeys * kPieces + T - 1) / T; ++i) {
+    const int q = tid + T * i;
+    if (q >= kKeys * kPieces) continue;
+    const int k = q / kPieces, id = ids[k];
+    const uint8_t* row = id >= 0 ? kv + (int64_t)id * kFp8RowBytes : zero_row;
+    // the wave's lanes fill 64 consecutive pieces from the first lane's
+    __builtin_amdgcn_global_load_lds(
+        (const __attribute__((address_space(1))) uint32_t*)(row + 16 * (q - k * kPieces)),
+        (__attribute__((address_space(3))) uint32_t*)(blk + 16 * (first + T * i)), 16, 0, 0);
+  }
+}
+
+__device__ __forceinline__ void wait_rows() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// As Fetch4::store's sanitize, on a block in LDS; ends with a barrier.
+template <int T>
+__device__ __forceinline__ void sanitize_rows(uint8_t* blk, int32_t* ids, int from) {
+  for (int q = threadIdx.x; q < kKeys * kPieces; q += T) {
+    const int k = q / kPieces, pc = q - k * kPieces;
+    if (k < from) continue;
+    u32x4* at = reinterpret_cast<u32x4*>(blk + 16 * q);
+    const u32x4 w = *at;
+    bool nan = false;
+    if (pc < 32) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) nan |= ((w[j / 4] >> (8 * (j % 4))) & 0x7fu) == 0x7fu;
+    } else if (pc == 32) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) nan |= (w[j] & 0x7f800000u) == 0x7f800000u;
+    } else {
+      nan = bad_bf16(w);
+    }
+    if (!nan) continue;
+    *at = u32x4{0u, 0u, 0u, 0u};
+    ids[k] = kBad;
+  }
+  __syncthreads();
+}
+
+template <int NP>
+__global__ void __launch_bounds__(128 * NP) decode_fp8_kernel(DecodeParams p) {
+  constexpr int T = 128 * NP;
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+  Lds8<NP>& s = *reinterpret_cast<Lds8<NP>*>(lds_raw);
+  Share sh;
+  if (!begin<true, NP>(p, s.lists, sh)) return;        // the whole workgroup
+  const int blocks = (sh.n + kKeys - 1) / kKeys;
+  if (blocks > 0) fetch_rows<T>(p.kv, s.lists.ids, s.blk[0]);
+  if (blocks > 1) fetch_rows<T>(p.kv, s.lists.ids + kKeys, s.blk[1]);
+  bf16x8 qb[18 - kQuerySteps8];
+  {
+    // in the order in which the keys are read: 16 values a lane for two steps
+    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, hi = l >> 5, half = w / NP;
+    const uint16_t* q =
+        p.q + ((int64_t)sh.item * p.rows + max(query_row<NP>(p, sh, tid), 0)) * kDim;
+#pragma unroll
+    for (int ks = 0; ks < 18; ++ks) {
+      const int at = ks < 16 ? half * 256 + (ks / 2) * 32 + 16 * hi + 8 * (ks % 2)
+                             : kLatent + half * 32 + (ks - 16) * 16 + 8 * hi;
+      const bf16x8 v = *reinterpret_cast<const bf16x8*>(q + at);
+      if (ks < 18 - kQuerySteps8)
+        qb[ks] = v;
+      else
+        s.qs[w][ks - 18 + kQuerySteps8][l] = v;
+    }
+  }
+  f32x16 o[8];                                 // O^T: dimensions 256 half + 32 dt + row, by column
+#pragma unroll
+  for (int dt = 0; dt < 8; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
+  float m_run = -INFINITY, l_run = 0.f;        // l_run: this lane's keys only
+  const float qk_scale = p.scale * kLog2e;
+  wait_rows();
+  __syncthreads();
+  int cur = 0;
+  for (int bi = 0; bi < blocks; ++bi) {
+    uint8_t* cb = s.blk[cur];
+    if ((bi + 1) * kKeys > sh.edge)
+      sanitize_rows<T>(cb, s.lists.ids + bi * kKeys, sh.edge - bi * kKeys);
+    const int tid = fresh_tid(), w = tid >> 6, l = tid & 63;
+    const int col = l & 31, hi = l >> 5, duo = w % NP, half = w / NP;
+    auto query = [&](int ks) {
+      return ks < 18 - kQuerySteps8 ? qb[ks] : s.qs[w][ks - 18 + kQuerySteps8][l];
+    };
+    // ---- this half's share of S^T: row (key) col of A is row `col` of the block
+    const uint8_t* krow = cb + col * kFp8RowBytes + half * 256 + 16 * hi;
+    const uint8_t* rrow = cb + col * kFp8RowBytes + kRope + half * 64 + 16 * hi;
+    // the scales of key 8 i + 4 hi + j, this half's two
+    const uint8_t* srow = cb + 4 * hi * kFp8RowBytes + kScales + 8 * half;
+    f32x16 sc;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sc[i] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+      sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+          *reinterpret_cast<const bf16x8*>(rrow + 32 * ks), query(16 + ks), sc, 0, 0, 0);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      f32x16 acc;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const u32x4 k = *reinterpret_cast<const u32x4*>(krow + 128 * t + 32 * c);
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp8x8(k[0], k[1]), query(8 * t + 2 * c), acc,
+                                                      0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp8x8(k[2], k[3]), query(8 * t + 2 * c + 1), acc,
+                                                      0, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float k = *reinterpret_cast<const float*>(
+            srow + (8 * (i / 4) + i % 4) * kFp8RowBytes + 4 * t);
+        sc[i] += acc[i] * k;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      s.xs[w][i][l] = f32x4{sc[4 * i], sc[4 * i + 1], sc[4 * i + 2], sc[4 * i + 3]};
+    // past this barrier: the scores and the next block's rows are complete, and
+    // every wave is done with the block before, whose buffer is filled next
+    wait_rows();
+    __syncthreads();
+    const int nxt = cur == 2 ? 0 : cur + 1;
+    if (bi + 2 < blocks)
+      fetch_rows<T>(p.kv, s.lists.ids + (bi + 2) * kKeys, s.blk[nxt == 2 ? 0 : nxt + 1]);
+    // ---- the other half's share (a sum of two: alike in both waves)
+    const int other = w < NP ? w + NP : w - NP;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 v = s.xs[other][i][l];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sc[4 * i + j] = (sc[4 * i + j] + v[j]) * qk_scale;
+    }
+    mask<true, NP>(s.lists, sh, bi, duo * 32 + col, hi, sc);
+    softmax(sc, m_run, l_run, o);
+    // ---- O^T += V^T P'^T, P' = p * scale of the latent tile.  Step ks covers
+    // keys 16 ks + 4 hi + {0..3, 8..11}, the ones this lane holds; lane c of a
+    // 16-lane group supplies row c / 2 of those and 8 dimensions
+    const int j8 = (l & 15) >> 1;
+    const uint8_t* vrow = cb + (4 * hi + j8 + (j8 < 4 ? 0 : 4)) * kFp8RowBytes + half * 256 +
+                          16 * ((l >> 4) & 1) + 8 * (l & 1);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
       bf16x8 pb[2];
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         u32x4 v;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float x[4];
-          if constexpr (FP4) {
+        for (int i = 0; i < 4; ++i) {
+          float x[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = pr[8 * ks + 4 * i + j];
-          } else {
-            const f32x4 k4 = *reinterpret_cast<const f32x4*>(
-                &cb.scale[2 * half + t][16 * ks + 8 * i + 4 * hi]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = pr[8 * ks + 4 * i + j] * k4[j];
+          for (int j = 0; j < 2; ++j) {
+            const int r = 8 * ks + 2 * i + j;
+            x[j] = sc[r] * *reinterpret_cast<const float*>(
+                               srow + (8 * (r / 4) + r % 4) * kFp8RowBytes + 4 * t);
           }
-          v[2 * i] = bf16_pair(x[0], x[1]);
-          v[2 * i + 1] = bf16_pair(x[2], x[3]);
+          v[i] = bf16_pair(x[0], x[1]);
         }
         pb[ks] = __builtin_bit_cast(bf16x8, v);
+        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
-      for (int d = 0; d < (FP4 ? 8 : 4); ++d) {
-        const int dt = 4 * t + d;
+      for (int d = 0; d < 4; ++d)
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          const u32x2 a = tr16_read(vrow + 16 * ks * kLatStride + 64 * dt);
-          const u32x2 b = tr16_read(vrow + (16 * ks + 8) * kLatStride + 64 * dt);
-          o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]}), pb[ks], o[dt], 0, 0, 0);
+          const u32x2 a = tr8_read(vrow + 16 * ks * kFp8RowBytes + 32 * (4 * t + d));
+          o[4 * t + d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp8x8(a[0], a[1]), pb[ks],
+                                                                 o[4 * t + d], 0, 0, 0);
         }
-      }
     }
-    __syncthreads();
+    cur = nxt;
+    __syncthreads();                           // the scores are read
   }
-
-  const int32_t m = query_row(fresh_tid());
-  if (m < 0) return;
-  l_run += __shfl_xor(l_run, 32);              // the same query row
-  const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-  const int d0 = half * 256 + 4 * hi;
-  const int64_t mrow = (int64_t)item * p.rows + m;
-  if (p.splits == 1) {
-    uint16_t* out = p.out + mrow * kLatent + d0;
-#pragma unroll
-    for (int dt = 0; dt < 8; ++dt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<u32x2*>(out + 32 * dt + 8 * i) =
-            u32x2{bf16_pair(o[dt][4 * i] * inv, o[dt][4 * i + 1] * inv),
-                  bf16_pair(o[dt][4 * i + 2] * inv, o[dt][4 * i + 3] * inv)};
-    if (half == 0 && hi == 0)
-      p.lse[mrow] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) / kLog2e;
-    return;
-  }
-  const int64_t ps = ((int64_t)item * p.splits + split) * p.rows + m;
-  if (half == 0 && hi == 0) {
-    p.part_ml[2 * ps] = m_run;
-    p.part_ml[2 * ps + 1] = l_run;
-  }
-  if (l_run == 0.f) return;                    // the merge does not read it
-  uint16_t* po = p.part_o + ps * kLatent + d0;
-#pragma unroll
-  for (int dt = 0; dt < 8; ++dt)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<f16x4*>(po + 32 * dt + 8 * i) =
-          f16x4{(_Float16)(o[dt][4 * i] * inv), (_Float16)(o[dt][4 * i + 1] * inv),
-                (_Float16)(o[dt][4 * i + 2] * inv), (_Float16)(o[dt][4 * i + 3] * inv)};
+  finish<NP>(p, sh, o, m_run, l_run);
 }
 
 // Merges the key splits of a query row, one wave a row: with w_s = 2^(m_s - M)
@@ -536,13 +738,11 @@ int64_t grid_of(const DecodeParams& p) {
   return ((int64_t)p.items * p.splits + 7) / 8 * 8 * p.row_tiles;
 }
 
-template <bool FP4, bool PAGED, int NP>
-hipError_t launch(const DecodeParams& p, hipStream_t stream) {
-  auto fn = decode_kernel<FP4, PAGED, NP>;
-  static std::atomic<uint64_t> raised{0};
+hipError_t launch(void (*fn)(DecodeParams), int threads, size_t lds, std::atomic<uint64_t>& raised,
+                  const DecodeParams& p, hipStream_t stream) {
   hipError_t e = allow_full_lds(reinterpret_cast<const void*>(fn), raised);
   if (e != hipSuccess) return e;
-  return launch_kernel(fn, dim3((uint32_t)grid_of(p)), dim3(128 * NP), sizeof(Lds<NP>), stream, p);
+  return launch_kernel(fn, dim3((uint32_t)grid_of(p)), dim3((uint32_t)threads), lds, stream, p);
 }
 
 }  // namespace
@@ -577,8 +777,12 @@ hipError_t launch_decode(DecodeParams p, bool fp4, bool paged, void* workspace,
     p.part_o = static_cast<uint16_t*>(workspace);
     p.part_ml = reinterpret_cast<float*>(p.part_o + (size_t)p.items * p.splits * p.rows * kLatent);
   }
-  hipError_t e = paged ? (fp4 ? launch<true, true, 4>(p, stream) : hipErrorNotSupported)
-                       : launch<true, false, 4>(p, stream);
+  constexpr int NP = kDecodeRows / 32;
+  static std::atomic<uint64_t> raised[3];
+  hipError_t e =
+      !paged ? launch(decode_fp4_kernel<false, NP>, 128 * NP, sizeof(Lds4<NP>), raised[0], p, stream)
+      : fp4  ? launch(decode_fp4_kernel<true, NP>, 128 * NP, sizeof(Lds4<NP>), raised[1], p, stream)
+             : launch(decode_fp8_kernel<NP>, 128 * NP, sizeof(Lds8<NP>), raised[2], p, stream);
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t rows = (int64_t)p.items * p.rows;
   return launch_kernel(decode_merge_kernel, dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, stream,
