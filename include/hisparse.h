@@ -532,6 +532,46 @@ hs_status hs_paged_mla_decode(const hs_layout* layout, const hs_batch* batch, in
 size_t hs_paged_mla_workspace_bytes(int32_t num_reqs, int32_t num_pos, int32_t num_heads,
                                     int32_t max_ctx);
 
+/*
+ * hs_mla_prefill -- latent attention in the expanded form, for chunks of new
+ * tokens against the cached context (a turn's prompt; the rows are written
+ * before, with hs_mla_append).  Request r's queries are rows q_start[r] ..
+ * q_start[r + 1] - 1 of q, its newest tokens: with n of them, query i sees the
+ * tokens t <= ctx_len[r] - n + i.  For head h and token t with latent values c
+ * and rope values, its row found as by hs_paged_mla_decode:
+ *   key = [w_kv[h][0..127] c, rope] (192), value = w_kv[h][128..255] c (128),
+ *   out = sum_t softmax(sm_scale * <q, key(t)>)_t value(t).
+ * Tokens without a row select nothing; a query that sees none gets zeros.  A
+ * token that a query does not see has no part in its output, whatever its row
+ * holds; one that it sees with a NaN or an infinity in its row makes it NaN.
+ * Arguments: q_start device int32 [R + 1], ascending, from 0 to num_q at most
+ * (rows of out that no request has keep their values); q device bf16
+ * [num_q][H][192] (128 values, then 64 rotated rope values); w_kv device bf16
+ * [H][256][512]; out device bf16 [num_q][H][128]; all three 16-byte aligned.
+ * num_kv: no smaller than the sum of ctx_len (requests' tokens past it, in
+ * order, are not attended to).  Uses batch->num_reqs, max_pages, block_table,
+ * ctx_len and kv_pool.  workspace: at least
+ * hs_mla_prefill_workspace_bytes(R, num_q, num_kv, H) bytes, 16-byte aligned,
+ * overwritten (the expanded keys and values: 512 bytes a token and head); calls
+ * sharing one must not overlap.
+ * Precision: products and sums in float32; the latent values (where a row's
+ * scale is no power of two), the expanded keys and values, the probabilities
+ * and out are rounded to bfloat16.
+ * Errors: HS_ERR_INVALID_ARGUMENT (null or misaligned pointers with work to
+ * do, a short workspace, negative sizes, num_heads < 1, a bad layer or
+ * layout), HS_ERR_UNSUPPORTED (another row_bytes, over 1,048,576 heads or
+ * requests, over 65,535 tiles of 128 tokens or queries), HS_ERR_LAUNCH.
+ */
+hs_status hs_mla_prefill(const hs_layout* layout, const hs_batch* batch, int32_t layer,
+                         const int32_t* q_start, int32_t num_q, int32_t num_kv, const uint16_t* q,
+                         int32_t num_heads, const uint16_t* w_kv, float sm_scale, uint16_t* out,
+                         void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace hs_mla_prefill needs for these sizes (0 where there is
+ * nothing to do, or for negative sizes). */
+size_t hs_mla_prefill_workspace_bytes(int32_t num_reqs, int32_t num_q, int32_t num_kv,
+                                      int32_t num_heads);
+
 /* A static English description of a status code. */
 const char* hs_status_string(hs_status status);
 

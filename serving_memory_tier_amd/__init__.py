@@ -21,14 +21,15 @@ from .api import (HostPool, append_of, batch_of, hs_gather, hs_host_alloc, hs_ho
                   hs_sparse_mla_workspace_bytes, hs_sparse_mla_decode_noalloc,
                   hs_sparse_mla_noalloc_max_workspace, hs_mla_append, hs_status_string, layout_of,
                   hs_sparse_mla_decode_fp4, hs_sparse_mla_fp4_workspace_bytes,
-                  hs_paged_mla_decode, hs_paged_mla_workspace_bytes)
+                  hs_paged_mla_decode, hs_paged_mla_workspace_bytes, hs_mla_prefill,
+                  hs_mla_prefill_workspace_bytes)
 
 __all__ = [
     "EXPORTS", "HS_OK", "HS_ERR_INVALID_ARGUMENT", "HS_ERR_UNSUPPORTED", "HS_ERR_LAUNCH",
     "HS_ERR_HIP", "HS_MAX_ENTRIES", "HS_MAX_HOT_CAPACITY", "HS_MAX_ROW_BYTES", "HS_FILL_SYNC_WORDS", "LIB_PATH",
     "HS_ROW_FP8", "HS_ROW_FP4", "HsLayout", "HsBatch", "HsAppend", "append_of", "hs_mla_append",
     "hs_sparse_mla_decode_fp4", "hs_sparse_mla_fp4_workspace_bytes", "hs_paged_mla_decode",
-    "hs_paged_mla_workspace_bytes",
+    "hs_paged_mla_workspace_bytes", "hs_mla_prefill", "hs_mla_prefill_workspace_bytes",
     "HsError", "HostPool", "lib", "layout_of", "batch_of", "hs_resolve", "hs_gather",
     "hs_offload_prefix_pages", "hs_plan_replay", "hs_resolve_grouped", "hs_resolve_decide",
     "hs_resolve_fetch",

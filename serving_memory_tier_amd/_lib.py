@@ -26,7 +26,8 @@ EXPORTS = ("hs_resolve", "hs_gather", "hs_offload_prefix_pages", "hs_plan_replay
            "hs_page_touch", "hs_resolve_in_place", "hs_sparse_mla_decode", "hs_sparse_mla_workspace_bytes",
            "hs_sparse_mla_decode_noalloc", "hs_sparse_mla_noalloc_max_workspace",
            "hs_mla_append", "hs_sparse_mla_decode_fp4", "hs_sparse_mla_fp4_workspace_bytes",
-           "hs_paged_mla_decode", "hs_paged_mla_workspace_bytes",
+           "hs_paged_mla_decode", "hs_paged_mla_workspace_bytes", "hs_mla_prefill",
+           "hs_mla_prefill_workspace_bytes",
            "hs_status_string", "hs_last_error", "hs_host_alloc", "hs_host_free",
            "hs_host_device_pointer")
 
@@ -102,6 +103,9 @@ def lib():
         L.hs_paged_mla_decode.argtypes = [lay, bat, i32, vp, i32, i32, i32, ctypes.c_float, vp, vp,
                                           vp, sz, vp]
         L.hs_paged_mla_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.hs_mla_prefill.argtypes = [lay, bat, i32, vp, i32, i32, vp, i32, vp, ctypes.c_float, vp,
+                                     vp, sz, vp]
+        L.hs_mla_prefill_workspace_bytes.argtypes = [i32, i32, i32, i32]
         L.hs_status_string.argtypes = [i32]
         L.hs_status_string.restype = ctypes.c_char_p
         L.hs_last_error.argtypes = []
@@ -117,5 +121,6 @@ def lib():
         L.hs_sparse_mla_noalloc_max_workspace.restype = sz
         L.hs_sparse_mla_fp4_workspace_bytes.restype = sz
         L.hs_paged_mla_workspace_bytes.restype = sz
+        L.hs_mla_prefill_workspace_bytes.restype = sz
         _lib = L
     return _lib

@@ -312,6 +312,26 @@ def hs_paged_mla_decode(layout: HsLayout, batch: HsBatch, layer: int, q, num_pos
         "hs_paged_mla_decode")
 
 
+def hs_mla_prefill_workspace_bytes(num_reqs: int, num_q: int, num_kv: int, num_heads: int) -> int:
+    return int(lib().hs_mla_prefill_workspace_bytes(num_reqs, num_q, num_kv, num_heads))
+
+
+def hs_mla_prefill(layout: HsLayout, batch: HsBatch, layer: int, q_start, num_q: int, num_kv: int,
+                   q, num_heads: int, w_kv, sm_scale: float, out, workspace, stream=None) -> None:
+    """q_start int32 [R + 1]; q bf16 [num_q, H, 192]; w_kv bf16 [H, 256, 512]; out bf16
+    [num_q, H, 128]; workspace: a tensor of hs_mla_prefill_workspace_bytes."""
+    _sized(q_start, "q_start", batch.num_reqs + 1)
+    _sized(q, "q", num_q * num_heads * 192)
+    _sized(w_kv, "w_kv", num_heads * 256 * 512)
+    _sized(out, "out", num_q * num_heads * 128)
+    ws, ws_bytes = _workspace(workspace)
+    _check(lib().hs_mla_prefill(
+        ctypes.byref(layout), ctypes.byref(batch), layer,
+        _operand(q_start, "q_start", (torch.int32,)), num_q, num_kv, _operand(q, "q", _BF16),
+        num_heads, _operand(w_kv, "w_kv", _BF16), sm_scale, _operand(out, "out", _BF16), ws,
+        ws_bytes, _stream(stream)), "hs_mla_prefill")
+
+
 def hs_host_alloc(nbytes: int) -> int:
     p = ctypes.c_void_p()
     _check(lib().hs_host_alloc(nbytes, ctypes.byref(p)), "hs_host_alloc")

@@ -186,4 +186,54 @@ size_t hs_paged_mla_workspace_bytes(int32_t num_reqs, int32_t num_pos, int32_t n
   return hs::plan_decode(p, max_ctx);
 }
 
+hs_status hs_mla_prefill(const hs_layout* layout, const hs_batch* batch, int32_t layer,
+                         const int32_t* q_start, int32_t num_q, int32_t num_kv, const uint16_t* q,
+                         int32_t num_heads, const uint16_t* w_kv, float sm_scale, uint16_t* out,
+                         void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  hs_status s = check_layout(layout);
+  if (s != HS_OK) return s;
+  if (!batch || layer < 0 || layer >= layout->num_layers) return HS_ERR_INVALID_ARGUMENT;
+  bool fp4 = false;
+  if ((s = row_format(layout, &fp4)) != HS_OK) return s;
+  if (batch->num_reqs < 0 || batch->max_pages < 1 || num_q < 0 || num_kv < 0 || num_heads < 1)
+    return HS_ERR_INVALID_ARGUMENT;
+  if (num_heads > kMaxRows || batch->num_reqs > kMaxRows) return HS_ERR_UNSUPPORTED;
+  if (batch->num_reqs == 0 || num_q == 0) return HS_OK;
+  if (!q_start || !q || !w_kv || !out || !batch->kv_pool || !batch->block_table || !batch->ctx_len)
+    return HS_ERR_INVALID_ARGUMENT;
+  if (!aligned16(batch->kv_pool) || !aligned16(q) || !aligned16(w_kv) || !aligned16(out))
+    return HS_ERR_INVALID_ARGUMENT;
+  hs::PrefillParams p{};
+  p.kv = batch->kv_pool + (int64_t)layer * layout->pool_layer_stride;
+  p.pool_rows = layout->pool_rows;
+  p.block_table = batch->block_table;
+  p.ctx_len = batch->ctx_len;
+  p.num_reqs = batch->num_reqs;
+  p.max_pages = batch->max_pages;
+  p.page_shift = log2i(layout->page_size);
+  p.q_start = q_start;
+  p.num_q = num_q;
+  p.num_kv = num_kv;
+  p.q = q;
+  p.heads = num_heads;
+  p.w = w_kv;
+  p.scale = sm_scale;
+  p.out = out;
+  const size_t need = hs::plan_prefill(p, workspace);
+  if (!workspace || workspace_bytes < need || !aligned16(workspace)) return HS_ERR_INVALID_ARGUMENT;
+  if (!hs::prefill_fits(p)) return HS_ERR_UNSUPPORTED;
+  return from_hip(hs::launch_prefill(p, fp4, stream), "MLA prefill launch");
+}
+
+size_t hs_mla_prefill_workspace_bytes(int32_t num_reqs, int32_t num_q, int32_t num_kv,
+                                      int32_t num_heads) {
+  if (num_reqs <= 0 || num_q <= 0 || num_kv < 0 || num_heads <= 0) return 0;
+  hs::PrefillParams p{};
+  p.num_reqs = num_reqs;
+  p.num_q = num_q;
+  p.num_kv = num_kv;
+  p.heads = num_heads;
+  return hs::plan_prefill(p, nullptr);
+}
+
 }  // extern "C"

@@ -46,6 +46,7 @@
 #include <atomic>
 
 #include "latent.h"
+#include "parts.h"
 
 namespace hs {
 namespace {
@@ -55,68 +56,6 @@ constexpr int kLatent = 512;
 constexpr int kDim = 576;
 constexpr int kSplitKeys = 2048;             // keys a split, at most: their row ids are in LDS
 constexpr int32_t kBad = -2;                 // in place of a fetched row's id: see Fetch4::store
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kStaleMax = 8.f;             // log2 of the largest unnormalised probability
-
-typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
-typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
-typedef __attribute__((ext_vector_type(16))) float f32x16;
-typedef __attribute__((ext_vector_type(4))) float f32x4;
-typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
-typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
-typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
-typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
-typedef __attribute__((ext_vector_type(4))) short s16x4;
-typedef __attribute__((ext_vector_type(2))) int i32x2;
-typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
-
-// Within each 16 lanes, lane c receives element c % 4 of the 8-byte vectors at
-// the addresses of lanes 4 j + c / 4, j = 0..3.
-__device__ __forceinline__ u32x2 tr16_read(const uint8_t* p) {
-  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                       (lds_s16x4*)(const_cast<uint8_t*>(p))));
-}
-
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
-}
-
-// Within each 16 lanes, lane c receives byte c % 8 of the 8-byte vectors at the
-// addresses of lanes 2 j + c / 8, j = 0..7.
-__device__ __forceinline__ u32x2 tr8_read(const uint8_t* p) {
-  return __builtin_bit_cast(
-      u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(const_cast<uint8_t*>(p))));
-}
-
-// Whether any of eight bfloat16 values is a NaN or an infinity.
-__device__ __forceinline__ bool bad_bf16(u32x4 w) {
-  bool bad = false;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    bad |= (w[j] & 0x7f800000u) == 0x7f800000u || (w[j] & 0x7f80u) == 0x7f80u;
-  return bad;
-}
-
-template <bool HI>
-__device__ __forceinline__ uint32_t fp8_pair(uint32_t w) {
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
-}
-
-// Eight E4M3 bytes as bfloat16, exactly.
-__device__ __forceinline__ bf16x8 fp8x8(uint32_t a, uint32_t b) {
-  return __builtin_bit_cast(
-      bf16x8, u32x4{fp8_pair<false>(a), fp8_pair<true>(a), fp8_pair<false>(b), fp8_pair<true>(b)});
-}
-
-// The thread's number, opaque to the compiler: what it addresses with it is
-// computed where it is used instead of held in registers over the loop.
-__device__ __forceinline__ int fresh_tid() {
-  int t = threadIdx.x;
-  asm volatile("" : "+v"(t));
-  return t;
-}
-
 // The lists every form keeps in LDS.
 template <int NP>
 struct Lists {
@@ -519,13 +458,9 @@ __device__ __forceinline__ void fetch_rows(const uint8_t* kv, const int32_t* ids
     const int k = q / kPieces, id = ids[k];
     const uint8_t* row = id >= 0 ? kv + (int64_t)id * kFp8RowBytes : zero_row;
     // the wave's lanes fill 64 consecutive pieces from the first lane's
-    __builtin_amdgcn_global_load_lds(
-        (const __attribute__((address_space(1))) uint32_t*)(row + 16 * (q - k * kPieces)),
-        (__attribute__((address_space(3))) uint32_t*)(blk + 16 * (first + T * i)), 16, 0, 0);
+    load_to_lds(row + 16 * (q - k * kPieces), blk + 16 * (first + T * i));
   }
 }
-
-__device__ __forceinline__ void wait_rows() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // As Fetch4::store's sanitize, on a block in LDS; ends with a barrier.
 template <int T>

@@ -70,4 +70,45 @@ bool decode_fits(const DecodeParams& p);
 hipError_t launch_decode(DecodeParams p, bool fp4, bool paged, void* workspace,
                          hipStream_t stream);
 
+// Expanded latent attention of chunks of new tokens (prefill.hip).
+struct PrefillParams {
+  const uint8_t* kv;        // one layer of the pool
+  int64_t pool_rows;
+  const int32_t* block_table;
+  const int32_t* ctx_len;
+  int32_t num_reqs, max_pages, page_shift;
+  const int32_t* q_start;   // [reqs + 1]
+  int32_t num_q, num_kv;    // queries; tokens of the workspace
+  const uint16_t* q;        // [num_q][heads][192]
+  int32_t heads;
+  const uint16_t* w;        // [heads][128 key + 128 value dimensions][512]
+  float scale;
+  uint16_t* out;            // [num_q][heads][128]
+  // set by plan_prefill
+  int32_t tile_rows, max_tiles;
+  int32_t* off;             // [reqs + 1]
+  int32_t* tile_off;        // [reqs + 1]
+  uint8_t* flags;           // [num_kv]
+  uint16_t* lat;            // [num_kv][512]
+  uint16_t* rope;           // [num_kv][64]
+  uint16_t* heads_kv;       // [heads][num_kv][256]
+
+  // Request r's first query and its queries, whatever q_start holds.
+  __device__ int32_t query_start(int32_t r) const {
+    const int32_t s = q_start[r];
+    return s < 0 ? 0 : s > num_q ? num_q : s;
+  }
+};
+
+__device__ inline int32_t query_count(const PrefillParams& p, int32_t r) {
+  const int32_t n = p.query_start(r + 1) - p.query_start(r);
+  return n < 0 ? 0 : n;
+}
+
+// Sets the launch shape and lays out the workspace (null: sizes only); its bytes.
+size_t plan_prefill(PrefillParams& p, void* workspace);
+// Whether a planned launch's grid is within the device's limits.
+bool prefill_fits(const PrefillParams& p);
+hipError_t launch_prefill(const PrefillParams& p, bool fp4, hipStream_t stream);
+
 }  // namespace hs

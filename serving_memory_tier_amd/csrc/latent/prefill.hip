@@ -1,0 +1,480 @@
+// Latent attention in the expanded form, for a chunk of new tokens against the
+// cached context: keys and values of every head from the latent rows,
+//   k_j = [W^K_h c_j, rope_j] (128 + 64),  v_j = W^V_h c_j (128),
+// then causal attention of 192-wide queries.  For n new tokens the absorbed
+// form costs 2 * 1088 FLOPs a (query, key, head), this one 2 * 320 and, once a
+// key and head, 2 * 512 * 256: it wins from some 350 new tokens on.
+//
+// Four launches: the offsets of the requests' tokens; the rows, brought out of
+// the paged pool as bfloat16 [token][512] and [token][64]; the expansion, a
+// matrix product to [head][token][128 + 128]; the attention.
+//
+// Rounding: latent values are exact in bfloat16 where a row's scales are powers
+// of two (as hs_mla_append writes them), rounded once otherwise; products and
+// sums in float32; the expanded keys and values, the probabilities and the
+// output are rounded to bfloat16, as a model that stores them would.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "latent.h"
+#include "parts.h"
+
+namespace hs {
+namespace {
+
+constexpr int kNope = 128, kRopeDim = 64, kVal = 128;
+constexpr int kQ = kNope + kRopeDim;         // 192
+constexpr int kHeadRow = kNope + kVal;       // 256 values a (head, token)
+
+// ------------------------------------------------------------- offsets
+
+// off[r]: the first workspace row of request r's tokens (its context, cut to
+// the table and to what num_kv leaves); tile_off[r]: its first query tile.
+__global__ void __launch_bounds__(1024) prefill_plan_kernel(PrefillParams p) {
+  __shared__ int64_t sums[2][1024];
+  __shared__ int64_t base[2];
+  const int tid = threadIdx.x;
+  if (tid < 2) base[tid] = 0;
+  for (int32_t r0 = 0; r0 < p.num_reqs; r0 += 1024) {
+    const int32_t r = r0 + tid;
+    int64_t n = 0, tiles = 0;
+    if (r < p.num_reqs) {
+      n = min((int64_t)max(p.ctx_len[r], 0), (int64_t)p.max_pages << p.page_shift);
+      tiles = (query_count(p, r) + p.tile_rows - 1) / p.tile_rows;
+    }
+    sums[0][tid] = n;
+    sums[1][tid] = tiles;
+    __syncthreads();
+    for (int d = 1; d < 1024; d *= 2) {
+      const int64_t a = tid >= d ? sums[0][tid - d] : 0, b = tid >= d ? sums[1][tid - d] : 0;
+      __syncthreads();
+      sums[0][tid] += a;
+      sums[1][tid] += b;
+      __syncthreads();
+    }
+    if (r < p.num_reqs) {
+      p.off[r + 1] = (int32_t)min((int64_t)p.num_kv, base[0] + sums[0][tid]);
+      p.tile_off[r + 1] = (int32_t)min((int64_t)p.max_tiles, base[1] + sums[1][tid]);
+    }
+    __syncthreads();
+    if (tid < 2) base[tid] += sums[tid][1023];
+    __syncthreads();
+  }
+  if (tid == 0) p.off[0] = p.tile_off[0] = 0;
+}
+
+// The last r with off[r] <= i, off ascending from 0 over n requests.
+__device__ __forceinline__ int32_t find(const int32_t* off, int32_t n, int32_t i) {
+  int32_t lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int32_t mid = (lo + hi + 1) / 2;
+    if (off[mid] <= i) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// ---------------------------------------------------------------- rows
+
+// One wave a token: its row's latent values and rope values as bfloat16.  A
+// token without a row, or whose row holds a NaN or an infinity, gets zeros and
+// a flag (1: none, 2: not finite): a value that some queries must not see
+// cannot reach them through a product with a probability of 0.
+template <bool FP4>
+__global__ void __launch_bounds__(256) prefill_rows_kernel(PrefillParams p) {
+  const int l = threadIdx.x & 63;
+  const int32_t i = (int32_t)(blockIdx.x * 4 + (threadIdx.x >> 6));
+  if (i >= p.off[p.num_reqs]) return;
+  const int32_t r = find(p.off, p.num_reqs, i);
+  const int32_t t = i - p.off[r];
+  const int32_t b = p.block_table[(int64_t)r * p.max_pages + (t >> p.page_shift)];
+  const bool there = b >= 0 && b < p.pool_rows >> p.page_shift;
+  u32x4 v = {0u, 0u, 0u, 0u}, rope = {0u, 0u, 0u, 0u};
+  bool bad = false;
+  if (there) {
+    const int32_t id = (b << p.page_shift) | (t & ((1 << p.page_shift) - 1));
+    if constexpr (FP4) {
+      const uint8_t* row = p.kv + (int64_t)id * kFp4RowBytes;
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(row + 4 * l);
+      const uint32_t sb = row[256 + l / 4];
+      const float s = __builtin_bit_cast(float, sb << 23);
+      bad = sb == 255u;
+      v = u32x4{
+          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)),
+          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
+          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
+          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
+      if (l < 8) rope = *reinterpret_cast<const u32x4*>(row + 272 + 16 * l);
+    } else {
+      const uint8_t* row = p.kv + (int64_t)id * kFp8RowBytes;
+      const u32x2 w = *reinterpret_cast<const u32x2*>(row + 8 * l);
+      const float s = *reinterpret_cast<const float*>(row + 512 + 4 * (l / 16));
+      const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[0], false);
+      const f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[0], true);
+      const f32x2 d = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[1], false);
+      const f32x2 e = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[1], true);
+      v = u32x4{bf16_pair(a[0] * s, a[1] * s), bf16_pair(c[0] * s, c[1] * s),
+                bf16_pair(d[0] * s, d[1] * s), bf16_pair(e[0] * s, e[1] * s)};
+      if (l < 8) rope = *reinterpret_cast<const u32x4*>(row + 528 + 16 * l);
+    }
+    bad |= bad_bf16(v) || bad_bf16(rope);
+    bad = __any(bad);
+  }
+  if (!there || bad) v = rope = u32x4{0u, 0u, 0u, 0u};
+  *reinterpret_cast<u32x4*>(p.lat + (int64_t)i * 512 + 8 * l) = v;
+  if (l < 8) *reinterpret_cast<u32x4*>(p.rope + (int64_t)i * kRopeDim + 8 * l) = rope;
+  if (l == 0) p.flags[i] = !there ? 1 : bad ? 2 : 0;
+}
+
+// ----------------------------------------------------------- expansion
+
+// [token][512] x [head][256][512]^T -> [head][token][256], a workgroup of 4
+// waves a tile of 128 tokens x one head's 256 dimensions, a wave 64 x 128 of
+// it; the contraction in 16 chunks of 32.  Chunks go straight into LDS, three
+// resident (one computed, one complete or on its way, one being left), one
+// barrier a chunk; 16-byte pieces of a row are exchanged by bits 2 and 3 of its
+// number, which puts 16 rows' fragments on distinct banks.  Two workgroups a
+// unit.  The grid runs over heads first: an XCD sees every eighth head, whose
+// weights (256 KB) stay in its L2 over the tokens' tiles.
+constexpr int kGemmM = 128, kGemmN = 256, kGemmK = 32;
+constexpr int kGemmThreads = 256;
+
+struct GemmLds {
+  union {
+    struct {
+      uint8_t a[kGemmM * 64];
+      uint8_t w[kGemmN * 64];
+    } chunk[3];
+    uint16_t out[kGemmM][kGemmN + 8];
+  };
+};
+
+__device__ __forceinline__ int gemm_slot(int row, int piece) {
+  return row * 64 + 16 * (piece ^ ((row >> 2) & 3));
+}
+
+// 16-byte pieces of `rows` rows of 32 values, from src rows row_bytes apart.
+template <int ROWS>
+__device__ __forceinline__ void gemm_fetch(const uint8_t* src, int64_t row_bytes, int32_t last,
+                                           uint8_t* dst) {
+  const int tid = threadIdx.x, first = __builtin_amdgcn_readfirstlane(tid);
+#pragma unroll
+  for (int i = 0; i < ROWS * 4 / kGemmThreads; ++i) {
+    const int q = tid + kGemmThreads * i, row = q >> 2;
+    const int piece = (q & 3) ^ ((row >> 2) & 3);
+    load_to_lds(src + (int64_t)min(row, last) * row_bytes + 16 * piece,
+                dst + 16 * (first + kGemmThreads * i));
+  }
+}
+
+__global__ void __launch_bounds__(kGemmThreads, 2) prefill_expand_kernel(PrefillParams p) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+  GemmLds& s = *reinterpret_cast<GemmLds*>(lds_raw);
+  const int head = blockIdx.x;
+  const int32_t m0 = (int32_t)blockIdx.y * kGemmM;
+  const int32_t total = p.off[p.num_reqs];
+  if (m0 >= total) return;
+  const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, col = l & 31, hi = l >> 5;
+  const int wm = (w & 1) * 64, wn = (w >> 1) * 128;
+  const uint8_t* a = reinterpret_cast<const uint8_t*>(p.lat + (int64_t)m0 * 512);
+  const uint8_t* b = reinterpret_cast<const uint8_t*>(p.w + (int64_t)head * kGemmN * 512);
+  const int32_t last = min(kGemmM, total - m0) - 1;
+  auto fetch = [&](int c) {
+    gemm_fetch<kGemmM>(a + c * 64, 1024, last, s.chunk[c % 3].a);
+    gemm_fetch<kGemmN>(b + c * 64, 1024, kGemmN - 1, s.chunk[c % 3].w);
+  };
+  f32x16 acc[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.f;
+  fetch(0);
+  fetch(1);
+  for (int c = 0; c < 512 / kGemmK; ++c) {
+    // chunk c is complete: all but the last fetched one
+    if (c + 1 < 512 / kGemmK)
+      asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+    else
+      wait_rows();
+    __syncthreads();
+    if (c + 2 < 512 / kGemmK) fetch(c + 2);
+    const uint8_t* ca = s.chunk[c % 3].a;
+    const uint8_t* cw = s.chunk[c % 3].w;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      bf16x8 fa[2], fb[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        fa[i] = *reinterpret_cast<const bf16x8*>(ca + gemm_slot(wm + 32 * i + col, 2 * ks + hi));
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        fb[j] = *reinterpret_cast<const bf16x8*>(cw + gemm_slot(wn + 32 * j + col, 2 * ks + hi));
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    }
+  }
+  // (W A^T): column = token, rows = dimensions 4 hi + 8 i + 0..3; through LDS so
+  // that the stores are whole rows
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<u32x2*>(&s.out[wm + 32 * i + col][wn + 32 * j + 8 * k + 4 * hi]) =
+            u32x2{bf16_pair(acc[i][j][4 * k], acc[i][j][4 * k + 1]),
+                  bf16_pair(acc[i][j][4 * k + 2], acc[i][j][4 * k + 3])};
+  __syncthreads();
+  uint16_t* out = p.heads_kv + ((int64_t)head * p.num_kv + m0) * kHeadRow;
+  for (int q = tid; q < kGemmM * 32; q += kGemmThreads) {
+    const int row = q >> 5, pc = q & 31;
+    if (row <= last)
+      *reinterpret_cast<u32x4*>(out + (int64_t)row * kHeadRow + 8 * pc) =
+          *reinterpret_cast<const u32x4*>(&s.out[row][8 * pc]);
+  }
+}
+
+// ----------------------------------------------------------- attention
+
+// A workgroup of NW waves takes 32 NW queries of one request and head, a wave
+// 32; keys in tiles of 64, two resident in LDS, the next on its way while one
+// is computed; one barrier a tile.  S^T (64 keys x 32 queries) is 24 MFMAs
+// 32x32x16 a wave, O^T (128 x 32) += V^T P^T 16; the probabilities are the B
+// operand from registers, V^T comes through the transposing LDS read.
+// The grid runs over heads first (an XCD sees every eighth head's keys), and
+// the last tiles, which see the most keys, come first.
+constexpr int kTile = 64;
+
+struct TileLds {
+  uint8_t nope[kTile * 256];                 // 16-byte piece c of row r at place c ^ (r & 15)
+  uint8_t rope[kTile * 128];                 // at c ^ (r / 2 & 7)
+  uint8_t val[kTile * 256];                  // at c ^ (r & 3) * 4
+};
+
+template <int NW>
+__device__ __forceinline__ void fetch_tile(const PrefillParams& p, const uint8_t* hkv,
+                                           const uint8_t* rope, int32_t k0, int32_t n, TileLds& s) {
+  constexpr int T = 64 * NW;
+  const int tid = threadIdx.x, first = __builtin_amdgcn_readfirstlane(tid);
+  // keys past the request's last one read the last: masked, and finite
+#pragma unroll
+  for (int i = 0; i < kTile * 16 / T; ++i) {
+    const int q = tid + T * i, row = q >> 4, c = q & 15;
+    const uint8_t* src = hkv + (int64_t)min(k0 + row, n - 1) * (kHeadRow * 2);
+    load_to_lds(src + 16 * (c ^ (row & 15)), s.nope + 16 * (first + T * i));
+    load_to_lds(src + 256 + 16 * (c ^ ((row & 3) * 4)), s.val + 16 * (first + T * i));
+  }
+#pragma unroll
+  for (int i = 0; i < kTile * 8 / T; ++i) {
+    const int q = tid + T * i, row = q >> 3, c = q & 7;
+    load_to_lds(rope + (int64_t)min(k0 + row, n - 1) * 128 + 16 * (c ^ ((row >> 1) & 7)),
+                s.rope + 16 * (first + T * i));
+  }
+}
+
+template <int NW>
+__global__ void __launch_bounds__(64 * NW, 2) prefill_attend_kernel(PrefillParams p) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+  TileLds* s = reinterpret_cast<TileLds*>(lds_raw);
+  const int head = blockIdx.x;
+  const int32_t tiles_all = p.tile_off[p.num_reqs];
+  const int32_t ti = tiles_all - 1 - (int32_t)blockIdx.y;
+  if (ti < 0) return;
+  const int32_t r = find(p.tile_off, p.num_reqs, ti);
+  const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, col = l & 31, hi = l >> 5;
+  const int32_t nq = query_count(p, r);
+  const int32_t q0 = (ti - p.tile_off[r]) * (32 * NW);          // first query of the tile
+  const int32_t n = p.off[r + 1] - p.off[r];                    // tokens at hand
+  const int32_t unseen = max(p.ctx_len[r], 0) - nq;             // query i sees i + 1 + unseen
+  auto sees = [&](int32_t i) { return max(0, min(n, unseen + i + 1)); };
+  const int32_t wq = q0 + 32 * w;                               // this wave's first query
+  const int32_t limit = sees(min(wq + col, nq - 1));
+  const int32_t keys = sees(min(q0 + 32 * NW, nq) - 1);         // of the workgroup
+  const int32_t mine = wq < nq ? sees(min(wq + 32, nq) - 1) : 0;  // of the wave
+  const int32_t least = wq < nq ? sees(wq) : 0;
+  const int64_t qrow = p.query_start(r) + min(wq + col, nq - 1);
+
+  bf16x8 qb[12];
+  {
+    const uint16_t* q = p.q + (qrow * p.heads + head) * kQ;
+#pragma unroll
+    for (int ks = 0; ks < 12; ++ks) qb[ks] = *reinterpret_cast<const bf16x8*>(q + 16 * ks + 8 * hi);
+  }
+  f32x16 o[4];
+#pragma unroll
+  for (int dt = 0; dt < 4; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
+  float m_run = -INFINITY, l_run = 0.f;
+  const float qk_scale = p.scale * kLog2e;
+  const int64_t at = p.off[r];
+  const uint8_t* hkv =
+      reinterpret_cast<const uint8_t*>(p.heads_kv + ((int64_t)head * p.num_kv + at) * kHeadRow);
+  const uint8_t* rope = reinterpret_cast<const uint8_t*>(p.rope + at * kRopeDim);
+  const uint8_t* flags = p.flags + at;
+  const int32_t count = (keys + kTile - 1) / kTile;
+  if (count > 0) fetch_tile<NW>(p, hkv, rope, 0, n, s[0]);
+  for (int32_t j = 0; j < count; ++j) {
+    const int32_t k0 = j * kTile;
+    wait_rows();
+    __syncthreads();                           // tile j is complete, tile j - 1 left
+    if (j + 1 < count) fetch_tile<NW>(p, hkv, rope, k0 + kTile, n, s[(j + 1) & 1]);
+    if (k0 >= mine) continue;                  // the wave's queries see nothing here
+    const TileLds& t = s[j & 1];
+    const uint8_t flag = k0 + l < n ? flags[k0 + l] : 1;
+    f32x16 sc[2];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sc[kt][i] = 0.f;
+      const int row = 32 * kt + col;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks)
+        sc[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            *reinterpret_cast<const bf16x8*>(t.nope + 256 * row + 16 * ((2 * ks + hi) ^ (row & 15))),
+            qb[ks], sc[kt], 0, 0, 0);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        sc[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            *reinterpret_cast<const bf16x8*>(t.rope + 128 * row +
+                                             16 * ((2 * ks + hi) ^ ((row >> 1) & 7))),
+            qb[8 + ks], sc[kt], 0, 0, 0);
+    }
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) sc[kt] *= qk_scale;
+    // ---- masks: keys without a row, keys past the query
+    const uint64_t gone = __ballot(flag == 1), bad = __ballot(flag == 2);
+    if (gone != 0 || bad != 0 || k0 + kTile > least) {
+      const int32_t left = limit - k0;
+      uint64_t seen = left >= kTile ? ~0ull : left <= 0 ? 0ull : (1ull << left) - 1ull;
+      seen &= ~gone;
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        const uint32_t see = (uint32_t)(seen >> (32 * kt)) >> (4 * hi);
+        const uint32_t nan = (uint32_t)(bad >> (32 * kt)) >> (4 * hi);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t bit = 1u << (8 * (i / 4) + i % 4);
+          if (nan & bit) sc[kt][i] = __builtin_nanf("");
+          if (!(see & bit)) sc[kt][i] = -INFINITY;
+        }
+      }
+    }
+    // ---- online softmax; the maximum is renewed only when it grows by 2^8
+    float mb = sc[0][0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) mb = fmaxf(mb, sc[i / 16][i % 16]);
+    mb = fmaxf(mb, __shfl_xor(mb, 32));
+    const bool grow = mb > m_run + kStaleMax;
+    const float m_new = grow ? mb : m_run;
+    const float alpha = grow ? __builtin_amdgcn_exp2f(m_run - m_new) : 1.f;
+    const float base = m_new == -INFINITY ? 0.f : m_new;
+    float ls = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      sc[i / 16][i % 16] = __builtin_amdgcn_exp2f(sc[i / 16][i % 16] - base);
+      ls += sc[i / 16][i % 16];
+    }
+    l_run = l_run * alpha + ls;
+    m_run = m_new;
+    if (__any(grow)) {
+#pragma unroll
+      for (int dt = 0; dt < 4; ++dt) o[dt] *= alpha;
+    }
+    // ---- O^T += V^T P^T: step ks covers keys 16 ks + 4 hi + {0..3, 8..11}
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      const f32x16& x = sc[ks / 2];
+      const int e = 8 * (ks % 2);
+      const bf16x8 pb = __builtin_bit_cast(
+          bf16x8, u32x4{bf16_pair(x[e], x[e + 1]), bf16_pair(x[e + 2], x[e + 3]),
+                        bf16_pair(x[e + 4], x[e + 5]), bf16_pair(x[e + 6], x[e + 7])});
+      const int sub = (l & 15) >> 2;           // the row this lane supplies: + 4 hi, and 8 on
+      const uint8_t* v0 = t.val + 256 * (16 * ks + 4 * hi + sub);
+#pragma unroll
+      for (int dt = 0; dt < 4; ++dt) {
+        const int c = (4 * dt + 2 * ((l >> 4) & 1) + ((l & 3) >> 1)) ^ (sub * 4);
+        const u32x2 a = tr16_read(v0 + 16 * c + 8 * (l & 1));
+        const u32x2 b = tr16_read(v0 + 8 * 256 + 16 * c + 8 * (l & 1));
+        o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]}), pb, o[dt], 0, 0, 0);
+      }
+    }
+  }
+  if (wq + col >= nq) return;
+  l_run += __shfl_xor(l_run, 32);
+  const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+  uint16_t* out = p.out + (qrow * p.heads + head) * kVal + 4 * hi;
+#pragma unroll
+  for (int dt = 0; dt < 4; ++dt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<u32x2*>(out + 32 * dt + 8 * i) =
+          u32x2{bf16_pair(o[dt][4 * i] * inv, o[dt][4 * i + 1] * inv),
+                bf16_pair(o[dt][4 * i + 2] * inv, o[dt][4 * i + 3] * inv)};
+}
+
+constexpr size_t kAlign = 256;
+size_t up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
+
+}  // namespace
+
+size_t plan_prefill(PrefillParams& p, void* workspace) {
+  // 8 waves a tile where the queries fill it
+  p.tile_rows = p.num_q >= 256 * (int64_t)p.num_reqs ? 256 : 128;
+  p.max_tiles = (int32_t)min((int64_t)INT32_MAX, (int64_t)p.num_q / p.tile_rows + p.num_reqs);
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  size_t n = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* q = at ? at + n : nullptr;
+    n += up(bytes);
+    return q;
+  };
+  const size_t R = p.num_reqs, kv = p.num_kv, H = p.heads;
+  p.off = reinterpret_cast<int32_t*>(take((R + 1) * 4));
+  p.tile_off = reinterpret_cast<int32_t*>(take((R + 1) * 4));
+  p.flags = take(kv);
+  p.lat = reinterpret_cast<uint16_t*>(take(kv * 512 * 2));
+  p.rope = reinterpret_cast<uint16_t*>(take(kv * kRopeDim * 2));
+  p.heads_kv = reinterpret_cast<uint16_t*>(take(H * kv * kHeadRow * 2));
+  return n;
+}
+
+bool prefill_fits(const PrefillParams& p) {
+  return p.max_tiles <= 65535 && (p.num_kv + kGemmM - 1) / kGemmM <= 65535;
+}
+
+hipError_t launch_prefill(const PrefillParams& p, bool fp4, hipStream_t stream) {
+  if (p.num_reqs == 0 || p.num_q == 0) return hipSuccess;
+  hipError_t e = launch_kernel(prefill_plan_kernel, dim3(1), dim3(1024), 0, stream, p);
+  if (e != hipSuccess) return e;
+  if (p.num_kv > 0) {
+    e = launch_kernel(fp4 ? prefill_rows_kernel<true> : prefill_rows_kernel<false>,
+                      dim3((uint32_t)((p.num_kv + 3) / 4)), dim3(256), 0, stream, p);
+    if (e != hipSuccess) return e;
+    static std::atomic<uint64_t> raised{0};
+    e = allow_full_lds(reinterpret_cast<const void*>(prefill_expand_kernel), raised);
+    if (e != hipSuccess) return e;
+    e = launch_kernel(prefill_expand_kernel,
+                      dim3((uint32_t)p.heads, (uint32_t)((p.num_kv + kGemmM - 1) / kGemmM)),
+                      dim3(kGemmThreads), sizeof(GemmLds), stream, p);
+    if (e != hipSuccess) return e;
+  }
+  static std::atomic<uint64_t> raised[2];
+  const bool big = p.tile_rows == 256;
+  auto fn = big ? prefill_attend_kernel<8> : prefill_attend_kernel<4>;
+  e = allow_full_lds(reinterpret_cast<const void*>(fn), raised[big]);
+  if (e != hipSuccess) return e;
+  return launch_kernel(fn, dim3((uint32_t)p.heads, (uint32_t)p.max_tiles),
+                       dim3((uint32_t)p.tile_rows * 2), 2 * sizeof(TileLds), stream, p);
+}
+
+}  // namespace hs
