@@ -271,7 +271,9 @@ struct Fetch4 {
       const uint8_t* row = kv + (int64_t)max(id[i], 0) * kFp4RowBytes;
       const int pc = (tid + T * i) % kLat;
       lat[i] = *reinterpret_cast<const u32x4*>(row + 16 * pc);
-      scale[i] = row[256 + pc];
+      // the word that holds the scale: a byte's load would be widened, and waited
+      // for, right here
+      scale[i] = *reinterpret_cast<const uint32_t*>(row + 256 + (pc & ~3));
       there |= (id[i] >= 0 ? 1u : 0u) << i;
     }
 #pragma unroll
@@ -294,7 +296,7 @@ struct Fetch4 {
     for (int i = 0; i < kLatRounds; ++i) {
       const int q = tid + T * i, k = q / kLat, pc = q % kLat;
       u32x4 w = (there >> i) & 1 ? lat[i] : u32x4{0u, 0u, 0u, 0u};
-      uint32_t sb = (there >> i) & 1 ? scale[i] : 127u;
+      uint32_t sb = (there >> i) & 1 ? (scale[i] >> (8 * (pc & 3))) & 255u : 127u;
       if (sanitize && k >= from && sb == 255u) {
         ids[k] = kBad;
         w = u32x4{0u, 0u, 0u, 0u};
