@@ -9,8 +9,8 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = ["resolve.hip", "copy.hip", "fetch.hip", "touch.hip", "attend.hip", "api.hip",
-           "latent/append.hip", "latent/decode.hip", "latent/prefill.hip",
-           "latent/api.hip"]
+           "latent/append.hip", "latent/decode.hip", "latent/narrow.hip",
+           "latent/prefill.hip", "latent/api.hip"]
 ARCH = "gfx950"
 
 # Packed-FP32 instructions are switched off for all HIP code (hipcc's host pass

@@ -45,97 +45,26 @@
 
 #include <atomic>
 
-#include "latent.h"
-#include "parts.h"
+#include "decode_parts.h"
 
 namespace hs {
 namespace {
 
-constexpr int kKeys = 32;                    // rows a block
-constexpr int kLatent = 512;
-constexpr int kDim = 576;
-constexpr int kSplitKeys = 2048;             // keys a split, at most: their row ids are in LDS
-constexpr int32_t kBad = -2;                 // in place of a fetched row's id: see Fetch4::store
-// The lists every form keeps in LDS.
-template <int NP>
-struct Lists {
-  int32_t ids[kSplitKeys];                   // row ids, -1 where there is none; kBad
-  int32_t mine[32 * NP];                     // keys of the split that a query row sees
-  uint32_t there[kSplitKeys / 32];           // a block's keys that have a row
-};
-
-// A workgroup's share: keys [lo, lo + n) of its item for query rows from row0.
-struct Share {
-  int32_t item, split, row0;
-  int64_t lo;
-  int n, edge;                               // the first query row sees the fewest keys, `edge`
-};
-
-// Finds the workgroup's share and stages its row ids; false for the grid's
-// rounding.  Ends with a barrier.
-template <bool PAGED, int NP>
-__device__ __forceinline__ bool begin(const DecodeParams& p, Lists<NP>& s, Share& sh) {
-  constexpr int T = 128 * NP;
-  // workgroup -> (item, split, row tile): the row tiles of one (item, split)
-  // are 8 workgroups apart, the XCD stride, so one's rows are in the other's L2
-  const int64_t L = blockIdx.x;
-  const int tile = (int)((L >> 3) % p.row_tiles);
-  const int64_t pair = L / (8 * p.row_tiles) * 8 + (L & 7);
-  if (pair >= (int64_t)p.items * p.splits) return false;
-  sh.item = (int32_t)(pair % p.items);
-  sh.split = (int32_t)(pair / p.items);
-  sh.row0 = tile * 32 * NP;
-  sh.lo = (int64_t)sh.split * p.keys_per_split;
-  const int tid = threadIdx.x, l = tid & 63;
-  const int32_t rows = min(32 * NP, p.rows - sh.row0);
-  int64_t keys, unseen;                      // a query row sees unseen + its position of the keys
-  if constexpr (PAGED) {
-    const int64_t ctx = max(p.ctx_len[sh.item], 0);
-    keys = min(ctx, (int64_t)p.max_keys);
-    unseen = ctx - p.positions + 1;
-  } else {
-    keys = unseen = p.top_k;
-  }
-  auto seen = [&](int32_t row) {
-    return (int)max((int64_t)0, min(p.keys_per_split,
-                                    min(keys, unseen + (sh.row0 + row) / p.heads) - sh.lo));
-  };
-  sh.n = seen(rows - 1);
-  sh.edge = seen(0);
-  if (tid < 32 * NP) s.mine[tid] = seen(min(tid, rows - 1));
-  for (int k = tid; k < (sh.n + 63) / 64 * 64; k += T) {
-    int32_t id = -1;
-    if (k < sh.n) {
-      if constexpr (PAGED) {
-        const int64_t t = sh.lo + k;
-        const int32_t b = p.block_table[(int64_t)sh.item * p.max_pages + (t >> p.page_shift)];
-        if (b >= 0 && b < p.pool_rows >> p.page_shift)
-          id = (b << p.page_shift) | (int32_t)(t & ((1 << p.page_shift) - 1));
-      } else {
-        id = p.row_ids[(int64_t)sh.item * p.top_k + sh.lo + k];
-        if (id >= p.pool_rows) id = -1;
-      }
-    }
-    s.ids[k] = id;
-    const uint64_t b = __ballot(id >= 0);
-    if (l == 0) s.there[k >> 5] = (uint32_t)b;
-    if (l == 32) s.there[k >> 5] = (uint32_t)(b >> 32);
-  }
-  __syncthreads();
-  return true;
-}
+// Waves w and w + 4 share a SIMD; they take different pairs, in opposite phases.
+__device__ __forceinline__ int duo_of(int w) { return (w & 1) + 2 * (w >> 2); }
+__device__ __forceinline__ int half_of(int w) { return (w >> 1) & 1; }
 
 // Thread t's query row of the item, or -1 past the last.
 template <int NP>
 __device__ __forceinline__ int32_t query_row(const DecodeParams& p, const Share& sh, int t) {
-  const int32_t m = sh.row0 + (t >> 6) % NP * 32 + (t & 31);
+  const int32_t m = sh.row0 + duo_of(t >> 6) * 32 + (t & 31);
   return m < p.rows ? m : -1;
 }
 
 // Masks a block's scores (keys without a row, and keys the row does not see)
 // where it has any to mask.
 template <bool PAGED, int NP>
-__device__ __forceinline__ void mask(const Lists<NP>& s, const Share& sh, int bi, int row, int hi,
+__device__ __forceinline__ void mask(const Lists<32 * NP>& s, const Share& sh, int bi, int row, int hi,
                                      f32x16& sc) {
   const uint32_t there = s.there[bi];
   if (there == 0xffffffffu && (bi + 1) * kKeys <= sh.edge) return;
@@ -180,7 +109,7 @@ __device__ __forceinline__ void softmax(f32x16& sc, float& m_run, float& l_run, 
 template <int NP>
 __device__ __forceinline__ void finish(const DecodeParams& p, const Share& sh, const f32x16 (&o)[8],
                                        float m_run, float l_run) {
-  const int tid = fresh_tid(), hi = (tid & 63) >> 5, half = (tid >> 6) / NP;
+  const int tid = fresh_tid(), hi = (tid & 63) >> 5, half = half_of(tid >> 6);
   const int32_t m = query_row<NP>(p, sh, tid);
   if (m < 0) return;
   l_run += __shfl_xor(l_run, 32);              // the same query row
@@ -237,7 +166,7 @@ struct Lds4 {
   Block4 blk[2];
   f32x4 xs[2 * NP][4][64];                   // a wave's partial scores
   bf16x8 qs[2 * NP][kQuerySteps][64];
-  Lists<NP> lists;
+  Lists<32 * NP> lists;
 };
 
 // A block on its way from the pool to LDS: 16 latent pieces a row (16 bytes,
@@ -333,11 +262,11 @@ __global__ void __launch_bounds__(128 * NP) decode_fp4_kernel(DecodeParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
   Lds4<NP>& s = *reinterpret_cast<Lds4<NP>*>(lds_raw);
   Share sh;
-  if (!begin<PAGED, NP>(p, s.lists, sh)) return;       // the whole workgroup
+  if (!begin<PAGED, 32 * NP>(p, s.lists, sh)) return;       // the whole workgroup
   bf16x8 qb[kQueryRegs];
   {
     // a lane past the last row takes row 0's queries; it writes nothing
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, hi = l >> 5, half = w / NP;
+    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, hi = l >> 5, half = half_of(w);
     const uint16_t* q =
         p.q + ((int64_t)sh.item * p.rows + max(query_row<NP>(p, sh, tid), 0)) * kDim;
 #pragma unroll
@@ -367,11 +296,21 @@ __global__ void __launch_bounds__(128 * NP) decode_fp4_kernel(DecodeParams p) {
     if (blocks > 1) f.load(p.kv, ids + kKeys);
   }
   __syncthreads();
+  const bool late = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) != 0;
+  if (late) __syncthreads();
   for (int bi = 0; bi < blocks; ++bi) {
     const Block4& cb = s.blk[bi & 1];
     const int tid = fresh_tid(), w = tid >> 6, l = tid & 63;
-    const int col = l & 31, hi = l >> 5, duo = w % NP, half = w / NP;
+    const int col = l & 31, hi = l >> 5, duo = duo_of(w), half = half_of(w);
     auto query = [&](int ks) { return ks < kQueryRegs ? qb[ks] : s.qs[w][ks - kQueryRegs][l]; };
+    auto next = [&]() {
+      if (bi + 1 < blocks) {
+        f.store(s.blk[(bi + 1) & 1], ids + (bi + 1) * kKeys, PAGED && (bi + 2) * kKeys > sh.edge,
+                sh.edge - (bi + 1) * kKeys);
+        if (bi + 2 < blocks) f.load(p.kv, ids + (bi + 2) * kKeys);
+      }
+    };
+    if (late) next();
     // ---- this half's share of S^T: row (key) col of A is row `col` of the block
     f32x16 sc;
 #pragma unroll
@@ -388,18 +327,14 @@ __global__ void __launch_bounds__(128 * NP) decode_fp4_kernel(DecodeParams p) {
       s.xs[w][i][l] = f32x4{sc[4 * i], sc[4 * i + 1], sc[4 * i + 2], sc[4 * i + 3]};
     __syncthreads();
     // ---- the other half's share (a sum of two: alike in both waves)
-    const int other = w < NP ? w + NP : w - NP;
+    const int other = w ^ 2;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f32x4 v = s.xs[other][i][l];
 #pragma unroll
       for (int j = 0; j < 4; ++j) sc[4 * i + j] = (sc[4 * i + j] + v[j]) * qk_scale;
     }
-    if (bi + 1 < blocks) {
-      f.store(s.blk[(bi + 1) & 1], ids + (bi + 1) * kKeys, PAGED && (bi + 2) * kKeys > sh.edge,
-              sh.edge - (bi + 1) * kKeys);
-      if (bi + 2 < blocks) f.load(p.kv, ids + (bi + 2) * kKeys);
-    }
+    if (!late) next();
     mask<PAGED, NP>(s.lists, sh, bi, duo * 32 + col, hi, sc);
     softmax(sc, m_run, l_run, o);
     // ---- O^T += V^T P^T.  Step ks covers keys 16 ks + 4 hi + {0..3, 8..11},
@@ -425,12 +360,12 @@ __global__ void __launch_bounds__(128 * NP) decode_fp4_kernel(DecodeParams p) {
       }
     __syncthreads();
   }
+  if (!late) __syncthreads();
   finish<NP>(p, sh, o, m_run, l_run);
 }
 
 // -------------------------------------------------------------- FP8 rows
 
-constexpr int kPieces = kFp8RowBytes / 16;   // 41
 constexpr int kScales = 512, kRope = 528;    // offsets in a row
 
 constexpr int kQuerySteps8 = 7;              // query fragments in LDS, the last
@@ -440,53 +375,19 @@ constexpr int kQuerySteps8 = 7;              // query fragments in LDS, the last
 template <int NP>
 struct Lds8 {
   uint8_t blk[3][kKeys * kFp8RowBytes];
+  float scale[2][4][kKeys];                  // the rows' scales, by latent tile
   f32x4 xs[2 * NP][4][64];                   // a wave's partial scores
   bf16x8 qs[2 * NP][kQuerySteps8][64];
-  Lists<NP> lists;
+  Lists<32 * NP> lists;
 };
 
-// What a key without a row reads.
-__device__ __attribute__((aligned(16))) uint8_t zero_row[kFp8RowBytes];
-
-// A block's rows from the pool straight into LDS, 16 bytes a lane; wait_rows()
-// and a barrier before they are read.
-template <int T>
-__device__ __forceinline__ void fetch_rows(const uint8_t* kv, const int32_t* ids, uint8_t* blk) {
-  const int tid = fresh_tid(), first = __builtin_amdgcn_readfirstlane(tid);
-#pragma unroll
-  for (int i = 0; i < (kKeys * kPieces + T - 1) / T; ++i) {
-    const int q = tid + T * i;
-    if (q >= kKeys * kPieces) continue;
-    const int k = q / kPieces, id = ids[k];
-    const uint8_t* row = id >= 0 ? kv + (int64_t)id * kFp8RowBytes : zero_row;
-    // the wave's lanes fill 64 consecutive pieces from the first lane's
-    load_to_lds(row + 16 * (q - k * kPieces), blk + 16 * (first + T * i));
-  }
-}
-
-// As Fetch4::store's sanitize, on a block in LDS; ends with a barrier.
-template <int T>
-__device__ __forceinline__ void sanitize_rows(uint8_t* blk, int32_t* ids, int from) {
-  for (int q = threadIdx.x; q < kKeys * kPieces; q += T) {
-    const int k = q / kPieces, pc = q - k * kPieces;
-    if (k < from) continue;
-    u32x4* at = reinterpret_cast<u32x4*>(blk + 16 * q);
-    const u32x4 w = *at;
-    bool nan = false;
-    if (pc < 32) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) nan |= ((w[j / 4] >> (8 * (j % 4))) & 0x7fu) == 0x7fu;
-    } else if (pc == 32) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) nan |= (w[j] & 0x7f800000u) == 0x7f800000u;
-    } else {
-      nan = bad_bf16(w);
-    }
-    if (!nan) continue;
-    *at = u32x4{0u, 0u, 0u, 0u};
-    ids[k] = kBad;
-  }
-  __syncthreads();
+// The scales of a block in LDS, by latent tile, so that a lane's keys' are read
+// four at a time.
+__device__ __forceinline__ void copy_scales(const uint8_t* blk, float (&scale)[4][kKeys]) {
+  const int tid = fresh_tid();
+  if (tid < 4 * kKeys)
+    scale[tid & 3][tid >> 2] =
+        *reinterpret_cast<const float*>(blk + (tid >> 2) * kFp8RowBytes + kScales + 4 * (tid & 3));
 }
 
 template <int NP>
@@ -495,14 +396,14 @@ __global__ void __launch_bounds__(128 * NP) decode_fp8_kernel(DecodeParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
   Lds8<NP>& s = *reinterpret_cast<Lds8<NP>*>(lds_raw);
   Share sh;
-  if (!begin<true, NP>(p, s.lists, sh)) return;        // the whole workgroup
+  if (!begin<true, 32 * NP>(p, s.lists, sh)) return;        // the whole workgroup
   const int blocks = (sh.n + kKeys - 1) / kKeys;
-  if (blocks > 0) fetch_rows<T>(p.kv, s.lists.ids, s.blk[0]);
-  if (blocks > 1) fetch_rows<T>(p.kv, s.lists.ids + kKeys, s.blk[1]);
+  if (blocks > 0) fetch_rows<false, T>(p.kv, s.lists.ids, s.blk[0]);
+  if (blocks > 1) fetch_rows<false, T>(p.kv, s.lists.ids + kKeys, s.blk[1]);
   bf16x8 qb[18 - kQuerySteps8];
   {
     // in the order in which the keys are read: 16 values a lane for two steps
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, hi = l >> 5, half = w / NP;
+    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, hi = l >> 5, half = half_of(w);
     const uint16_t* q =
         p.q + ((int64_t)sh.item * p.rows + max(query_row<NP>(p, sh, tid), 0)) * kDim;
 #pragma unroll
@@ -524,22 +425,21 @@ __global__ void __launch_bounds__(128 * NP) decode_fp8_kernel(DecodeParams p) {
   float m_run = -INFINITY, l_run = 0.f;        // l_run: this lane's keys only
   const float qk_scale = p.scale * kLog2e;
   wait_rows();
+  if (blocks > 0 && kKeys > sh.edge) sanitize_rows<false, T>(s.blk[0], s.lists.ids, sh.edge);
+  __syncthreads();
+  copy_scales(s.blk[0], s.scale[0]);
   __syncthreads();
   int cur = 0;
   for (int bi = 0; bi < blocks; ++bi) {
     uint8_t* cb = s.blk[cur];
-    if ((bi + 1) * kKeys > sh.edge)
-      sanitize_rows<T>(cb, s.lists.ids + bi * kKeys, sh.edge - bi * kKeys);
     const int tid = fresh_tid(), w = tid >> 6, l = tid & 63;
-    const int col = l & 31, hi = l >> 5, duo = w % NP, half = w / NP;
+    const int col = l & 31, hi = l >> 5, duo = duo_of(w), half = half_of(w);
     auto query = [&](int ks) {
       return ks < 18 - kQuerySteps8 ? qb[ks] : s.qs[w][ks - 18 + kQuerySteps8][l];
     };
     // ---- this half's share of S^T: row (key) col of A is row `col` of the block
     const uint8_t* krow = cb + col * kFp8RowBytes + half * 256 + 16 * hi;
     const uint8_t* rrow = cb + col * kFp8RowBytes + kRope + half * 64 + 16 * hi;
-    // the scales of key 8 i + 4 hi + j, this half's two
-    const uint8_t* srow = cb + 4 * hi * kFp8RowBytes + kScales + 8 * half;
     f32x16 sc;
 #pragma unroll
     for (int i = 0; i < 16; ++i) sc[i] = 0.f;
@@ -562,10 +462,11 @@ __global__ void __launch_bounds__(128 * NP) decode_fp8_kernel(DecodeParams p) {
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float k = *reinterpret_cast<const float*>(
-            srow + (8 * (i / 4) + i % 4) * kFp8RowBytes + 4 * t);
-        sc[i] += acc[i] * k;
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 k4 =
+            *reinterpret_cast<const f32x4*>(&s.scale[bi & 1][2 * half + t][8 * i + 4 * hi]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[4 * i + j] += acc[4 * i + j] * k4[j];
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -575,12 +476,16 @@ __global__ void __launch_bounds__(128 * NP) decode_fp8_kernel(DecodeParams p) {
     // past this barrier: the scores and the next block's rows are complete, and
     // every wave is done with the block before, whose buffer is filled next
     wait_rows();
-    __syncthreads();
     const int nxt = cur == 2 ? 0 : cur + 1;
+    if (bi + 1 < blocks && (bi + 2) * kKeys > sh.edge)
+      sanitize_rows<false, T>(s.blk[nxt], s.lists.ids + (bi + 1) * kKeys,
+                              sh.edge - (bi + 1) * kKeys);
+    __syncthreads();
+    copy_scales(s.blk[nxt], s.scale[(bi + 1) & 1]);    // (past the last block: for nobody)
     if (bi + 2 < blocks)
-      fetch_rows<T>(p.kv, s.lists.ids + (bi + 2) * kKeys, s.blk[nxt == 2 ? 0 : nxt + 1]);
+      fetch_rows<false, T>(p.kv, s.lists.ids + (bi + 2) * kKeys, s.blk[nxt == 2 ? 0 : nxt + 1]);
     // ---- the other half's share (a sum of two: alike in both waves)
-    const int other = w < NP ? w + NP : w - NP;
+    const int other = w ^ 2;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f32x4 v = s.xs[other][i][l];
@@ -602,15 +507,12 @@ __global__ void __launch_bounds__(128 * NP) decode_fp8_kernel(DecodeParams p) {
       for (int ks = 0; ks < 2; ++ks) {
         u32x4 v;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int r = 8 * ks + 2 * i + j;
-            x[j] = sc[r] * *reinterpret_cast<const float*>(
-                               srow + (8 * (r / 4) + r % 4) * kFp8RowBytes + 4 * t);
-          }
-          v[i] = bf16_pair(x[0], x[1]);
+        for (int i = 0; i < 2; ++i) {
+          const f32x4 k4 = *reinterpret_cast<const f32x4*>(
+              &s.scale[bi & 1][2 * half + t][16 * ks + 8 * i + 4 * hi]);
+          const int e = 8 * ks + 4 * i;
+          v[2 * i] = bf16_pair(sc[e] * k4[0], sc[e + 1] * k4[1]);
+          v[2 * i + 1] = bf16_pair(sc[e + 2] * k4[2], sc[e + 3] * k4[3]);
         }
         pb[ks] = __builtin_bit_cast(bf16x8, v);
         __builtin_amdgcn_sched_barrier(0);
@@ -654,14 +556,21 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(DecodeParams p) {
       const float ls = p.part_ml[2 * ps + 1];
       if (ls != 0.f) wgt = exp2f(p.part_ml[2 * ps] - M) * ls;     // NaN stays NaN
     }
-    for (int j = 0; j < min(64, p.splits - s0); ++j) {
-      const float x = __shfl(wgt, j);
-      if (x == 0.f) continue;                  // nothing seen there: not written
-      sum += x;
-      const f16x8 h = *reinterpret_cast<const f16x8*>(
-          p.part_o + (ps0 + (int64_t)(s0 + j) * p.rows) * kLatent + 8 * l);
+    // eight splits' loads at a time; one that saw nothing was not written
+    for (int j0 = 0; j0 < min(64, p.splits - s0); j0 += 8) {
+      f16x8 h[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += x * (float)h[i];
+      for (int j = 0; j < 8; ++j)
+        h[j] = *reinterpret_cast<const f16x8*>(
+            p.part_o + (ps0 + (int64_t)min(s0 + j0 + j, p.splits - 1) * p.rows) * kLatent + 8 * l);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x = __shfl(wgt, j0 + j);   // 0 past the last split
+        if (x == 0.f) continue;
+        sum += x;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += x * (float)h[j][i];
+      }
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -671,32 +580,59 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(DecodeParams p) {
   if (l == 0) p.lse[mrow] = sum == 0.f ? -INFINITY : (M + log2f(sum)) / kLog2e;
 }
 
-int64_t grid_of(const DecodeParams& p) {
-  return ((int64_t)p.items * p.splits + 7) / 8 * 8 * p.row_tiles;
-}
-
 hipError_t launch(void (*fn)(DecodeParams), int threads, size_t lds, std::atomic<uint64_t>& raised,
                   const DecodeParams& p, hipStream_t stream) {
   hipError_t e = allow_full_lds(reinterpret_cast<const void*>(fn), raised);
   if (e != hipSuccess) return e;
-  return launch_kernel(fn, dim3((uint32_t)grid_of(p)), dim3((uint32_t)threads), lds, stream, p);
+  return launch_kernel(fn, dim3((uint32_t)decode_grid(p)), dim3((uint32_t)threads), lds, stream, p);
+}
+
+hipError_t launch_decode_wide(const DecodeParams& p, bool fp4, bool paged, hipStream_t stream) {
+  constexpr int NP = kDecodeRows / 32, T = 128 * NP;
+  static std::atomic<uint64_t> raised[3];
+  return !paged ? launch(decode_fp4_kernel<false, NP>, T, sizeof(Lds4<NP>), raised[0], p, stream)
+         : fp4  ? launch(decode_fp4_kernel<true, NP>, T, sizeof(Lds4<NP>), raised[1], p, stream)
+                : launch(decode_fp8_kernel<NP>, T, sizeof(Lds8<NP>), raised[2], p, stream);
 }
 
 }  // namespace
 
-// The workgroups of a launch to aim for: one round of the chip's 256 units.
-constexpr int64_t kDecodeGroups = 256;
-constexpr int64_t kDecodeMaxSplits = 64;   // below the splits that kSplitKeys asks for
+// In block times (about 3 us): a workgroup's start and end, a merge's launch, and
+// the rows whose partial outputs (2 KB written and read) take one.
+constexpr int kStartBlocks = 4, kMergeBlocks = 2;
+constexpr double kMergeRows = 7000;
+
+int64_t decode_grid(const DecodeParams& p) {
+  return ((int64_t)p.items * p.splits + 7) / 8 * 8 * p.row_tiles;
+}
 
 size_t plan_decode(DecodeParams& p, int64_t keys) {
-  p.row_tiles = (p.rows + kDecodeRows - 1) / kDecodeRows;
+  p.tile_rows = p.rows <= 16 ? 16 : p.rows <= 32 ? 32 : kDecodeRows;
+  p.row_tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
+  // Key splits: the fewest block times over the rounds of the chip that the
+  // workgroups take (256 units, two narrow workgroups each), with some block
+  // times a workgroup for its start and end, and a merge's launch and traffic
   const int64_t base = (int64_t)p.items * p.row_tiles;
   const int64_t blocks = (keys + kKeys - 1) / kKeys;
-  int64_t splits = base > 0 ? (kDecodeGroups + base - 1) / base : 1;
-  splits = min(splits, kDecodeMaxSplits);
-  splits = max(splits, (blocks * kKeys + kSplitKeys - 1) / kSplitKeys);
-  splits = max((int64_t)1, min(splits, blocks));
-  const int64_t per = (blocks + splits - 1) / splits;          // blocks a split, at most kSplitKeys
+  const int64_t slots = p.tile_rows == kDecodeRows ? 256 : 512;
+  const int64_t least = (blocks * kKeys + kDecodeSplitKeys - 1) / kDecodeSplitKeys;
+  int64_t best = 1;
+  double best_t = 1e300;
+  for (int r = 0; r <= 4; ++r) {               // as many as fill r rounds; 0: as few as may be
+    int64_t n = r > 0 && base > 0 ? r * slots / base : 1;
+    n = n < least ? least : n;
+    n = n > blocks ? blocks : n;
+    if (n < 1) n = 1;
+    const int64_t per = (blocks + n - 1) / n;
+    if (per > 0) n = (blocks + per - 1) / per;
+    const double t = (double)((base * n + slots - 1) / slots) * (per + kStartBlocks) +
+                     (n > 1 ? kMergeBlocks + (double)p.items * p.rows * n / kMergeRows : 0.0);
+    if (t < best_t) {
+      best_t = t;
+      best = n;
+    }
+  }
+  const int64_t per = (blocks + best - 1) / best;              // blocks a split
   p.splits = (int32_t)(per > 0 ? (blocks + per - 1) / per : 1);
   p.keys_per_split = per * kKeys;
   // per (item, split, row): 512 half-precision values and two floats
@@ -704,7 +640,7 @@ size_t plan_decode(DecodeParams& p, int64_t keys) {
 }
 
 bool decode_fits(const DecodeParams& p) {
-  return grid_of(p) <= INT32_MAX && (int64_t)p.items * p.rows <= 4 * (int64_t)INT32_MAX;
+  return decode_grid(p) <= INT32_MAX && (int64_t)p.items * p.rows <= 4 * (int64_t)INT32_MAX;
 }
 
 hipError_t launch_decode(DecodeParams p, bool fp4, bool paged, void* workspace,
@@ -714,12 +650,8 @@ hipError_t launch_decode(DecodeParams p, bool fp4, bool paged, void* workspace,
     p.part_o = static_cast<uint16_t*>(workspace);
     p.part_ml = reinterpret_cast<float*>(p.part_o + (size_t)p.items * p.splits * p.rows * kLatent);
   }
-  constexpr int NP = kDecodeRows / 32;
-  static std::atomic<uint64_t> raised[3];
-  hipError_t e =
-      !paged ? launch(decode_fp4_kernel<false, NP>, 128 * NP, sizeof(Lds4<NP>), raised[0], p, stream)
-      : fp4  ? launch(decode_fp4_kernel<true, NP>, 128 * NP, sizeof(Lds4<NP>), raised[1], p, stream)
-             : launch(decode_fp8_kernel<NP>, 128 * NP, sizeof(Lds8<NP>), raised[2], p, stream);
+  const hipError_t e = p.tile_rows == kDecodeRows ? launch_decode_wide(p, fp4, paged, stream)
+                                                  : launch_decode_narrow(p, fp4, paged, stream);
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t rows = (int64_t)p.items * p.rows;
   return launch_kernel(decode_merge_kernel, dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, stream,

@@ -1,0 +1,150 @@
+// What the two absorbed latent attention kernels share: a workgroup's share of
+// the work, its row ids, and rows on their way into LDS.
+#pragma once
+
+#include "latent.h"
+#include "parts.h"
+
+namespace hs {
+namespace {
+
+constexpr int kKeys = 32;                    // rows a block
+constexpr int kLatent = 512;
+constexpr int kDim = 576;
+constexpr int32_t kBad = -2;                 // in place of a fetched row's id: see sanitize_rows
+
+// The lists of a workgroup of ROWS query rows.
+template <int ROWS>
+struct Lists {
+  int32_t ids[kDecodeSplitKeys];                   // row ids, -1 where there is none; kBad
+  int32_t mine[ROWS];                        // keys of the split that a query row sees
+  uint32_t there[kDecodeSplitKeys / 32];           // a block's keys that have a row
+};
+
+// A workgroup's share: keys [lo, lo + n) of its item for query rows from row0.
+struct Share {
+  int32_t item, split, row0;
+  int64_t lo;
+  int n, edge;                               // the first query row sees the fewest keys, `edge`
+};
+
+// Finds the workgroup's share and stages its row ids; false for the grid's
+// rounding.  Ends with a barrier.
+template <bool PAGED, int ROWS>
+__device__ __forceinline__ bool begin(const DecodeParams& p, Lists<ROWS>& s, Share& sh) {
+  // workgroup -> (item, split, row tile): the row tiles of one (item, split)
+  // are 8 workgroups apart, the XCD stride, so one's rows are in the other's L2
+  const int64_t L = blockIdx.x;
+  const int tile = (int)((L >> 3) % p.row_tiles);
+  const int64_t pair = L / (8 * p.row_tiles) * 8 + (L & 7);
+  if (pair >= (int64_t)p.items * p.splits) return false;
+  sh.item = (int32_t)(pair % p.items);
+  sh.split = (int32_t)(pair / p.items);
+  sh.row0 = tile * ROWS;
+  sh.lo = (int64_t)sh.split * p.keys_per_split;
+  const int tid = threadIdx.x, l = tid & 63;
+  const int32_t rows = min(ROWS, p.rows - sh.row0);
+  int64_t keys, unseen;                      // a query row sees unseen + its position of the keys
+  if constexpr (PAGED) {
+    const int64_t ctx = max(p.ctx_len[sh.item], 0);
+    keys = min(ctx, (int64_t)p.max_keys);
+    unseen = ctx - p.positions + 1;
+  } else {
+    keys = unseen = p.top_k;
+  }
+  auto seen = [&](int32_t row) {
+    return (int)max((int64_t)0, min(p.keys_per_split,
+                                    min(keys, unseen + (sh.row0 + row) / p.heads) - sh.lo));
+  };
+  sh.n = seen(rows - 1);
+  sh.edge = seen(0);
+  for (int i = tid; i < ROWS; i += blockDim.x) s.mine[i] = seen(min(i, rows - 1));
+  for (int k = tid; k < (sh.n + 63) / 64 * 64; k += blockDim.x) {
+    int32_t id = -1;
+    if (k < sh.n) {
+      if constexpr (PAGED) {
+        const int64_t t = sh.lo + k;
+        const int32_t b = p.block_table[(int64_t)sh.item * p.max_pages + (t >> p.page_shift)];
+        if (b >= 0 && b < p.pool_rows >> p.page_shift)
+          id = (b << p.page_shift) | (int32_t)(t & ((1 << p.page_shift) - 1));
+      } else {
+        id = p.row_ids[(int64_t)sh.item * p.top_k + sh.lo + k];
+        if (id >= p.pool_rows) id = -1;
+      }
+    }
+    s.ids[k] = id;
+    const uint64_t b = __ballot(id >= 0);
+    if (l == 0) s.there[k >> 5] = (uint32_t)b;
+    if (l == 32) s.there[k >> 5] = (uint32_t)(b >> 32);
+  }
+  __syncthreads();
+  return true;
+}
+
+// What a key without a row reads.
+__device__ __attribute__((aligned(16))) uint8_t zero_row[kFp8RowBytes];
+
+template <bool FP4>
+struct Row {
+  static constexpr int kBytes = FP4 ? kFp4RowBytes : kFp8RowBytes;
+  static constexpr int kPieces = kBytes / 16;
+  static constexpr int kLatPieces = FP4 ? 16 : 32;
+  static constexpr int kScales = FP4 ? 256 : 512;
+  static constexpr int kRope = kScales + 16;
+};
+
+// A block's rows from the pool straight into LDS, 16 bytes a lane; wait_rows()
+// and a barrier before they are read.
+template <bool FP4, int T>
+__device__ __forceinline__ void fetch_rows(const uint8_t* kv, const int32_t* ids, uint8_t* raw) {
+  using R = Row<FP4>;
+  const int tid = fresh_tid(), first = __builtin_amdgcn_readfirstlane(tid);
+#pragma unroll
+  for (int i = 0; i < (kKeys * R::kPieces + T - 1) / T; ++i) {
+    const int q = tid + T * i;
+    if (kKeys * R::kPieces % T != 0 && q >= kKeys * R::kPieces) continue;
+    const int k = q / R::kPieces, id = ids[k];
+    const uint8_t* row = id >= 0 ? kv + (int64_t)id * R::kBytes : zero_row;
+    // the wave's lanes fill 64 consecutive pieces from the first lane's
+    load_to_lds(row + 16 * (q - k * R::kPieces), raw + 16 * (first + T * i));
+  }
+}
+
+// Rows from `from` on are seen by some query rows and masked for others, where
+// a probability of 0 times a NaN or an infinity would be NaN: pieces that hold
+// one become zeros and their row's id, no longer needed, kBad: its scores are
+// NaN for the query rows that see it.  On the pieces that this thread loaded
+// and waited for.
+template <bool FP4, int T>
+__device__ __forceinline__ void sanitize_rows(uint8_t* raw, int32_t* ids, int from) {
+  using R = Row<FP4>;
+  for (int q = threadIdx.x; q < kKeys * R::kPieces; q += T) {
+    const int k = q / R::kPieces, pc = q - k * R::kPieces;
+    if (k < from) continue;
+    u32x4* at = reinterpret_cast<u32x4*>(raw + 16 * q);
+    const u32x4 w = *at;
+    bool nan = false;
+    if (pc < R::kLatPieces) {
+      if (!FP4) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) nan |= ((w[j / 4] >> (8 * (j % 4))) & 0x7fu) == 0x7fu;
+      }
+    } else if (pc == R::kLatPieces) {
+      if (FP4) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) nan |= ((w[j / 4] >> (8 * (j % 4))) & 0xffu) == 0xffu;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) nan |= (w[j] & 0x7f800000u) == 0x7f800000u;
+      }
+    } else {
+      nan = bad_bf16(w);
+    }
+    if (!nan) continue;
+    *at = u32x4{0u, 0u, 0u, 0u};
+    ids[k] = kBad;
+  }
+}
+
+}  // namespace
+}  // namespace hs

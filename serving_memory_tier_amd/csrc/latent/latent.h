@@ -37,7 +37,8 @@ hipError_t launch_append(AppendParams p, bool fp4, bool interleaved, hipStream_t
 
 // Absorbed latent attention (decode.hip): M query rows an item, 576 wide, over
 // the item's keys; 512-wide bfloat16 outputs.
-constexpr int kDecodeRows = 128;           // query rows a workgroup
+constexpr int kDecodeRows = 128;           // query rows a workgroup (16 or 32: narrow.hip)
+constexpr int kDecodeSplitKeys = 2048;     // keys a split, at most: their row ids are in LDS
 
 struct DecodeParams {
   const uint8_t* kv;        // one layer of the pool
@@ -57,7 +58,7 @@ struct DecodeParams {
   uint16_t* out;            // [items][rows][512]
   float* lse;               // [items][rows]
   // set by plan_decode and launch_decode
-  int32_t row_tiles, splits;
+  int32_t tile_rows, row_tiles, splits;  // query rows a workgroup; their tiles
   int64_t keys_per_split;   // a multiple of 32
   uint16_t* part_o;         // [items][splits][rows][512] IEEE half, normalised
   float* part_ml;           // [items][splits][rows][2] (maximum, sum)
@@ -65,6 +66,8 @@ struct DecodeParams {
 
 // Sets the launch shape for items of about `keys` keys; returns the workspace's bytes.
 size_t plan_decode(DecodeParams& p, int64_t keys);
+int64_t decode_grid(const DecodeParams& p);
+hipError_t launch_decode_narrow(const DecodeParams& p, bool fp4, bool paged, hipStream_t stream);
 // Whether a planned launch's grid is within the device's limits.
 bool decode_fits(const DecodeParams& p);
 hipError_t launch_decode(DecodeParams p, bool fp4, bool paged, void* workspace,

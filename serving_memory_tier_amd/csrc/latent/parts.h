@@ -62,6 +62,19 @@ __device__ __forceinline__ bf16x8 fp8x8(uint32_t a, uint32_t b) {
       bf16x8, u32x4{fp8_pair<false>(a), fp8_pair<true>(a), fp8_pair<false>(b), fp8_pair<true>(b)});
 }
 
+// The two E2M1 values of byte B of a word times a power of two, as bfloat16,
+// exactly (an infinite scale: NaN).
+template <int B>
+__device__ __forceinline__ uint32_t fp4_pair(uint32_t w, float scale = 1.f) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, B));
+}
+
+// Eight E2M1 values times a power of two.
+__device__ __forceinline__ bf16x8 fp4x8(uint32_t w, float scale) {
+  return __builtin_bit_cast(bf16x8, u32x4{fp4_pair<0>(w, scale), fp4_pair<1>(w, scale),
+                                          fp4_pair<2>(w, scale), fp4_pair<3>(w, scale)});
+}
+
 // The thread's number, opaque to the compiler: what it addresses with it is
 // computed where it is used instead of held in registers over the loop.
 __device__ __forceinline__ int fresh_tid() {
