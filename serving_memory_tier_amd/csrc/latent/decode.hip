@@ -85,18 +85,18 @@ __device__ __forceinline__ void softmax(f32x16& sc, float& m_run, float& l_run, 
   float mb = sc[0];
 #pragma unroll
   for (int i = 1; i < 16; ++i) mb = fmaxf(mb, sc[i]);
-  mb = fmaxf(mb, __shfl_xor(mb, 32));
+  mb = max_halves(mb);
   const bool grow = mb > m_run + kStaleMax;
   const float m_new = grow ? mb : m_run;
   const float alpha = grow ? __builtin_amdgcn_exp2f(m_run - m_new) : 1.f;
   const float base = m_new == -INFINITY ? 0.f : m_new;    // nothing seen yet: exp2(-inf) = 0
-  float ls = 0.f;
+  float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     sc[i] = __builtin_amdgcn_exp2f(sc[i] - base);
-    ls += sc[i];
+    ls[i % 4] += sc[i];
   }
-  l_run = l_run * alpha + ls;
+  l_run = l_run * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
   m_run = m_new;
   if (__any(grow)) {
 #pragma unroll
@@ -147,9 +147,11 @@ __device__ __forceinline__ void finish(const DecodeParams& p, const Share& sh, c
 
 // ------------------------------------------------------------ 4-bit rows
 
-// Row strides in LDS: 1072 bytes (latent) and 144 (rope), 3 and 9 sixteen-byte
-// units modulo the banks: 16 consecutive rows' fragments fall on distinct
-// banks, and the rows of a transposing read do not overlap.
+// Converted rows in LDS: 1072 bytes apart (3 sixteen-byte units modulo the 16 of
+// the banks), rope rows 144 (9).  Within a row, unit u = 4 pc + j (piece pc's j-th,
+// 8 values) lies at unit 16 j + (pc ^ 4 j): the 16 lanes that write one j of a
+// row's pieces, the 16 rows of a key fragment and the 4 rows x 4 units of a
+// transposing read each fall on distinct banks.
 constexpr int kLatStride = 1072;
 constexpr int kRopeStride = 144;
 // Of a wave's 18 query fragments, the last are kept in LDS.
@@ -182,17 +184,21 @@ struct Fetch4 {
   u32x4 rope[kRopeRounds];
   uint32_t scale[kLatRounds];
   uint32_t there;                                              // bit a piece: its row is there
+  int32_t id[kLatRounds + kRopeRounds];
 
-  __device__ __forceinline__ void load(const uint8_t* kv, const int32_t* ids) {
+  __device__ __forceinline__ void load_ids(const int32_t* ids) {
     const int tid = fresh_tid();
-    int32_t id[kLatRounds + kRopeRounds];
 #pragma unroll
     for (int i = 0; i < kLatRounds; ++i) id[i] = ids[(tid + T * i) / kLat];
 #pragma unroll
     for (int i = 0; i < kRopeRounds; ++i) {
       const int q = tid + T * i;
-      id[kLatRounds + i] = q < kKeys * kRope ? ids[q / kRope] : -1;
+      id[kLatRounds + i] = ids[q < kKeys * kRope ? q / kRope : 0];
     }
+  }
+
+  __device__ __forceinline__ void load(const uint8_t* kv) {
+    const int tid = fresh_tid();
     there = 0;
 #pragma unroll
     for (int i = 0; i < kLatRounds; ++i) {
@@ -232,10 +238,10 @@ struct Fetch4 {
         sb = 127u;
       }
       const float s = __builtin_bit_cast(float, sb << 23);     // 255: infinity, whose product is NaN
-      uint8_t* dst = b.lat + k * kLatStride + 64 * pc;
+      uint8_t* dst = b.lat + k * kLatStride;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<u32x4*>(dst + 16 * j) = u32x4{
+        *reinterpret_cast<u32x4*>(dst + 256 * j + ((16 * pc) ^ (64 * j))) = u32x4{
             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 0)),
             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 1)),
             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 2)),
@@ -291,9 +297,13 @@ __global__ void __launch_bounds__(128 * NP) decode_fp4_kernel(DecodeParams p) {
   const int blocks = (sh.n + kKeys - 1) / kKeys;
   Fetch4<T> f;
   if (blocks > 0) {
-    f.load(p.kv, ids);
+    f.load_ids(ids);
+    f.load(p.kv);
     f.store(s.blk[0], ids, PAGED && kKeys > sh.edge, sh.edge);
-    if (blocks > 1) f.load(p.kv, ids + kKeys);
+    if (blocks > 1) {
+      f.load_ids(ids + kKeys);
+      f.load(p.kv);
+    }
   }
   __syncthreads();
   const bool late = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) != 0;
@@ -305,9 +315,10 @@ __global__ void __launch_bounds__(128 * NP) decode_fp4_kernel(DecodeParams p) {
     auto query = [&](int ks) { return ks < kQueryRegs ? qb[ks] : s.qs[w][ks - kQueryRegs][l]; };
     auto next = [&]() {
       if (bi + 1 < blocks) {
+        if (bi + 2 < blocks) f.load_ids(ids + (bi + 2) * kKeys);
         f.store(s.blk[(bi + 1) & 1], ids + (bi + 1) * kKeys, PAGED && (bi + 2) * kKeys > sh.edge,
                 sh.edge - (bi + 1) * kKeys);
-        if (bi + 2 < blocks) f.load(p.kv, ids + (bi + 2) * kKeys);
+        if (bi + 2 < blocks) f.load(p.kv);
       }
     };
     if (late) next();
@@ -315,13 +326,35 @@ __global__ void __launch_bounds__(128 * NP) decode_fp4_kernel(DecodeParams p) {
     f32x16 sc;
 #pragma unroll
     for (int i = 0; i < 16; ++i) sc[i] = 0.f;
-    const uint8_t* krow = cb.lat + col * kLatStride + half * 512 + 16 * hi;
+    // step ks reads unit 32 half + 2 ks + hi: ks = 8 a + 2 t + b
+    const uint8_t* krow = cb.lat + col * kLatStride + 256 * hi;
     const uint8_t* rrow = cb.rope + col * kRopeStride + half * 64 + 16 * hi;
+    const uint8_t* kbase[2][2];
 #pragma unroll
-    for (int ks = 0; ks < 18; ++ks)
-      sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-          *reinterpret_cast<const bf16x8*>(ks < 16 ? krow + 32 * ks : rrow + 32 * (ks - 16)),
-          query(ks), sc, 0, 0, 0);
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) kbase[a][b] = krow + 512 * b + 128 * (half ^ b) + 64 * (hi ^ a);
+    constexpr int kC = 4;                      // steps whose fragments are read under the last ones' products
+    bf16x8 kf[2][kC];
+    auto read_keys = [&](int c) {
+#pragma unroll
+      for (int j = 0; j < kC; ++j) {
+        const int ks = kC * c + j;
+        if (ks < 18)
+          kf[c & 1][j] = *reinterpret_cast<const bf16x8*>(ks < 16 ? kbase[ks >> 3][ks & 1] + 16 * ((ks >> 1) & 3)
+                                                         : rrow + 32 * (ks - 16));
+      }
+    };
+    read_keys(0);
+#pragma unroll
+    for (int c = 0; c < (18 + kC - 1) / kC; ++c) {
+      if (kC * (c + 1) < 18) read_keys(c + 1);
+#pragma unroll
+      for (int j = 0; j < kC; ++j)
+        if (kC * c + j < 18)
+          sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[c & 1][j], query(kC * c + j), sc, 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       s.xs[w][i][l] = f32x4{sc[4 * i], sc[4 * i + 1], sc[4 * i + 2], sc[4 * i + 3]};
@@ -340,8 +373,11 @@ __global__ void __launch_bounds__(128 * NP) decode_fp4_kernel(DecodeParams p) {
     // ---- O^T += V^T P^T.  Step ks covers keys 16 ks + 4 hi + {0..3, 8..11},
     // the ones this lane holds; lane c of a 16-lane group supplies row c / 4
     // and 4 dimensions of each transposing read
-    const uint8_t* vrow = cb.lat + (4 * hi + ((l & 15) >> 2)) * kLatStride + half * 512 +
-                          32 * ((l >> 4) & 1) + 8 * (l & 3);
+    // of row c / 4, unit 32 half + 4 dt + j
+    const int j = (l >> 3 & 2) + (l >> 1 & 1);
+    const uint8_t* vrow = cb.lat + (4 * hi + ((l & 15) >> 2)) * kLatStride + 256 * j +
+                          128 * (half ^ (j >> 1)) + 8 * (l & 1);
+    const uint8_t* vbase[2] = {vrow + 64 * (j & 1), vrow + 64 * (~j & 1)};
     bf16x8 pb[2];
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
@@ -349,15 +385,24 @@ __global__ void __launch_bounds__(128 * NP) decode_fp4_kernel(DecodeParams p) {
           bf16x8, u32x4{bf16_pair(sc[8 * ks], sc[8 * ks + 1]), bf16_pair(sc[8 * ks + 2], sc[8 * ks + 3]),
                         bf16_pair(sc[8 * ks + 4], sc[8 * ks + 5]),
                         bf16_pair(sc[8 * ks + 6], sc[8 * ks + 7])});
+    u32x2 vf[3][4];
+    auto read_values = [&](int dt) {
 #pragma unroll
-    for (int dt = 0; dt < 8; ++dt)
+      for (int j = 0; j < 4; ++j) vf[dt % 3][j] = tr16_read(vbase[dt >> 2] + 8 * j * kLatStride + 16 * (dt & 3));
+    };
+    read_values(0);
+    read_values(1);
+#pragma unroll
+    for (int dt = 0; dt < 8; ++dt) {
+      if (dt + 2 < 8) read_values(dt + 2);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        const u32x2 a = tr16_read(vrow + 16 * ks * kLatStride + 64 * dt);
-        const u32x2 b = tr16_read(vrow + (16 * ks + 8) * kLatStride + 64 * dt);
+        const u32x2 a = vf[dt % 3][2 * ks], b = vf[dt % 3][2 * ks + 1];
         o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
             __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]}), pb[ks], o[dt], 0, 0, 0);
       }
+      __builtin_amdgcn_sched_barrier(0);
+    }
     __syncthreads();
   }
   if (!late) __syncthreads();
@@ -587,8 +632,9 @@ hipError_t launch(void (*fn)(DecodeParams), int threads, size_t lds, std::atomic
   return launch_kernel(fn, dim3((uint32_t)decode_grid(p)), dim3((uint32_t)threads), lds, stream, p);
 }
 
-hipError_t launch_decode_wide(const DecodeParams& p, bool fp4, bool paged, hipStream_t stream) {
-  constexpr int NP = kDecodeRows / 32, T = 128 * NP;
+template <int NP>
+hipError_t launch_wide(const DecodeParams& p, bool fp4, bool paged, hipStream_t stream) {
+  constexpr int T = 128 * NP;
   static std::atomic<uint64_t> raised[3];
   return !paged ? launch(decode_fp4_kernel<false, NP>, T, sizeof(Lds4<NP>), raised[0], p, stream)
          : fp4  ? launch(decode_fp4_kernel<true, NP>, T, sizeof(Lds4<NP>), raised[1], p, stream)
@@ -607,14 +653,14 @@ int64_t decode_grid(const DecodeParams& p) {
 }
 
 size_t plan_decode(DecodeParams& p, int64_t keys) {
-  p.tile_rows = p.rows <= 16 ? 16 : p.rows <= 32 ? 32 : kDecodeRows;
+  p.tile_rows = p.rows <= 16 ? 16 : p.rows <= 32 ? 32 : p.rows <= 64 ? 64 : 128;
   p.row_tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
   // Key splits: the fewest block times over the rounds of the chip that the
   // workgroups take (256 units, two narrow workgroups each), with some block
   // times a workgroup for its start and end, and a merge's launch and traffic
   const int64_t base = (int64_t)p.items * p.row_tiles;
   const int64_t blocks = (keys + kKeys - 1) / kKeys;
-  const int64_t slots = p.tile_rows == kDecodeRows ? 256 : 512;
+  const int64_t slots = p.tile_rows >= 64 ? 256 : 512;
   const int64_t least = (blocks * kKeys + kDecodeSplitKeys - 1) / kDecodeSplitKeys;
   int64_t best = 1;
   double best_t = 1e300;
@@ -650,8 +696,9 @@ hipError_t launch_decode(DecodeParams p, bool fp4, bool paged, void* workspace,
     p.part_o = static_cast<uint16_t*>(workspace);
     p.part_ml = reinterpret_cast<float*>(p.part_o + (size_t)p.items * p.splits * p.rows * kLatent);
   }
-  const hipError_t e = p.tile_rows == kDecodeRows ? launch_decode_wide(p, fp4, paged, stream)
-                                                  : launch_decode_narrow(p, fp4, paged, stream);
+  const hipError_t e = p.tile_rows == 128  ? launch_wide<4>(p, fp4, paged, stream)
+                       : p.tile_rows == 64 ? launch_wide<2>(p, fp4, paged, stream)
+                                           : launch_decode_narrow(p, fp4, paged, stream);
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t rows = (int64_t)p.items * p.rows;
   return launch_kernel(decode_merge_kernel, dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, stream,

@@ -37,7 +37,6 @@ hipError_t launch_append(AppendParams p, bool fp4, bool interleaved, hipStream_t
 
 // Absorbed latent attention (decode.hip): M query rows an item, 576 wide, over
 // the item's keys; 512-wide bfloat16 outputs.
-constexpr int kDecodeRows = 128;           // query rows a workgroup (16 or 32: narrow.hip)
 constexpr int kDecodeSplitKeys = 2048;     // keys a split, at most: their row ids are in LDS
 
 struct DecodeParams {

@@ -75,6 +75,13 @@ __device__ __forceinline__ bf16x8 fp4x8(uint32_t w, float scale) {
                                           fp4_pair<2>(w, scale), fp4_pair<3>(w, scale)});
 }
 
+// The larger of a lane's value and that of the lane 32 away.
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x),
+                                                  __builtin_bit_cast(uint32_t, x), false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+
 // The thread's number, opaque to the compiler: what it addresses with it is
 // computed where it is used instead of held in registers over the loop.
 __device__ __forceinline__ int fresh_tid() {
