@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(128 * NP) decode_fp8_kernel(DecodeParams p) {
     if (bi + 1 < blocks && (bi + 2) * kKeys > sh.edge)
       sanitize_rows<false, T>(s.blk[nxt], s.lists.ids + (bi + 1) * kKeys,
                               sh.edge - (bi + 1) * kKeys);
-    __syncthreads();
+    lds_barrier();
     copy_scales(s.blk[nxt], s.scale[(bi + 1) & 1]);    // (past the last block: for nobody)
     if (bi + 2 < blocks)
       fetch_rows<false, T>(p.kv, s.lists.ids + (bi + 2) * kKeys, s.blk[nxt == 2 ? 0 : nxt + 1]);
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(128 * NP) decode_fp8_kernel(DecodeParams p) {
         }
     }
     cur = nxt;
-    __syncthreads();                           // the scores are read
+    lds_barrier();                             // the scores are read
   }
   finish<NP>(p, sh, o, m_run, l_run);
 }

@@ -72,6 +72,8 @@ bool decode_fits(const DecodeParams& p);
 hipError_t launch_decode(DecodeParams p, bool fp4, bool paged, void* workspace,
                          hipStream_t stream);
 
+constexpr int kPrefillMaxSplits = 16;
+
 // Expanded latent attention of chunks of new tokens (prefill.hip).
 struct PrefillParams {
   const uint8_t* kv;        // one layer of the pool
@@ -87,7 +89,9 @@ struct PrefillParams {
   float scale;
   uint16_t* out;            // [num_q][heads][128]
   // set by plan_prefill
-  int32_t tile_rows, max_tiles;
+  int32_t tile_rows, max_tiles, splits;
+  uint16_t* part_o;         // [splits][num_q][heads][128] IEEE half, normalised
+  float* part_ml;           // [splits][num_q][heads][2] (maximum, sum)
   int32_t* off;             // [reqs + 1]
   int32_t* tile_off;        // [reqs + 1]
   uint8_t* flags;           // [num_kv]

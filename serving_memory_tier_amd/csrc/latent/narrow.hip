@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_narrow_kernel(DecodeParams
     wait_rows();                               // this block's, asked for a block or two ago
     if (PAGED && (bi + 1) * kKeys > sh.edge)
       sanitize_rows<FP4, kThreads>(raw, ids + bi * kKeys, sh.edge - bi * kKeys);
-    __syncthreads();                           // complete; and the block before is done with
+    lds_barrier();                             // complete; and the block before is done with
     const int ahead = L::kBufs - 1;
     if (bi + ahead < blocks)
       fetch_rows<FP4, kThreads>(p.kv, ids + (bi + ahead) * kKeys,
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_narrow_kernel(DecodeParams
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) s.xs[w][rt][mt][l] = sc[rt][mt];
-    __syncthreads();
+    lds_barrier();
     float x[RT][8];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {

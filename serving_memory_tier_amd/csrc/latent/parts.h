@@ -91,14 +91,35 @@ __device__ __forceinline__ int fresh_tid() {
 }
 
 // 16 bytes a lane from the pool straight into LDS: a wave's lanes fill 1024
-// consecutive bytes from `base`, which is the same in all of them.
+// consecutive bytes from `base`, which is the same in all of them.  Written out
+// because the compiler waits for its own form of this load before every
+// transposing LDS read that follows; here wait_rows() and a barrier order them.
+// It has no register output, and the compiler's waits for its other loads only
+// become longer by loads that it does not count.  (M0 has no other user here: LDS
+// accesses need none, and no register array is indexed at run time.)
 __device__ __forceinline__ void load_to_lds(const uint8_t* src, uint8_t* base) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)src,
-                                   (__attribute__((address_space(3))) uint32_t*)base, 16, 0, 0);
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)base;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(src)
+               : "memory");
 }
 
-// Waits for this wave's loads into LDS; a barrier makes them every wave's.
-__device__ __forceinline__ void wait_rows() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// A barrier that leaves loads into LDS on their way (__syncthreads would wait
+// for all of them); this wave's other LDS accesses are done.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Waits for this wave's loads into LDS (and its others: the compiler knows this
+// wait and adds none behind it); a barrier makes them every wave's.
+__device__ __forceinline__ void wait_rows() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0f70);          // vmcnt(0), the other counters at their largest
+  asm volatile("" ::: "memory");
+}
 
 }  // namespace
 }  // namespace hs

@@ -5,9 +5,10 @@
 // form costs 2 * 1088 FLOPs a (query, key, head), this one 2 * 320 and, once a
 // key and head, 2 * 512 * 256: it wins from some 350 new tokens on.
 //
-// Four launches: the offsets of the requests' tokens; the rows, brought out of
-// the paged pool as bfloat16 [token][512] and [token][64]; the expansion, a
-// matrix product to [head][token][128 + 128]; the attention.
+// Launches: the rows, brought out of the paged pool as bfloat16 [token][512] and
+// [token][64] (with the offsets of the requests' tokens); the expansion, a matrix
+// product to [head][token][128 + 128]; the attention; and a merge where it
+// splits the keys.
 //
 // Rounding: latent values are exact in bfloat16 where a row's scales are powers
 // of two (as hs_mla_append writes them), rounded once otherwise; products and
@@ -32,7 +33,29 @@ constexpr int kHeadRow = kNope + kVal;       // 256 values a (head, token)
 // ------------------------------------------------------------- offsets
 
 // off[r]: the first workspace row of request r's tokens (its context, cut to
-// the table and to what num_kv leaves); tile_off[r]: its first query tile.
+// the table and to what num_kv leaves); tile_off[r]: its first query tile.  Up to
+// 64 requests, the rows' kernel finds them itself (a wave's lanes a request each)
+// and writes them for the launches behind it; more have a launch of their own.
+constexpr int kInlineReqs = 64;
+
+__device__ __forceinline__ int64_t context(const PrefillParams& p, int32_t r) {
+  return min((int64_t)max(p.ctx_len[r], 0), (int64_t)p.max_pages << p.page_shift);
+}
+
+__device__ __forceinline__ int64_t query_tiles(const PrefillParams& p, int32_t r) {
+  return (query_count(p, r) + p.tile_rows - 1) / p.tile_rows;
+}
+
+__device__ __forceinline__ int64_t wave_sums(int64_t n) {      // of this lane and those before
+  const int l = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int64_t a = __shfl_up(n, d);
+    if (l >= d) n += a;
+  }
+  return n;
+}
+
 __global__ void __launch_bounds__(1024) prefill_plan_kernel(PrefillParams p) {
   __shared__ int64_t sums[2][1024];
   __shared__ int64_t base[2];
@@ -42,8 +65,8 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(PrefillParams p) {
     const int32_t r = r0 + tid;
     int64_t n = 0, tiles = 0;
     if (r < p.num_reqs) {
-      n = min((int64_t)max(p.ctx_len[r], 0), (int64_t)p.max_pages << p.page_shift);
-      tiles = (query_count(p, r) + p.tile_rows - 1) / p.tile_rows;
+      n = context(p, r);
+      tiles = query_tiles(p, r);
     }
     sums[0][tid] = n;
     sums[1][tid] = tiles;
@@ -86,9 +109,27 @@ template <bool FP4>
 __global__ void __launch_bounds__(256) prefill_rows_kernel(PrefillParams p) {
   const int l = threadIdx.x & 63;
   const int32_t i = (int32_t)(blockIdx.x * 4 + (threadIdx.x >> 6));
-  if (i >= p.off[p.num_reqs]) return;
-  const int32_t r = find(p.off, p.num_reqs, i);
-  const int32_t t = i - p.off[r];
+  int32_t r, t;
+  if (p.num_reqs <= kInlineReqs) {
+    const int64_t end = min((int64_t)p.num_kv, wave_sums(l < p.num_reqs ? context(p, l) : 0));
+    if (blockIdx.x == 0 && threadIdx.x < 64) {
+      const int64_t tiles = min((int64_t)p.max_tiles,
+                                wave_sums(l < p.num_reqs ? query_tiles(p, l) : 0));
+      if (l < p.num_reqs) {
+        p.off[l + 1] = (int32_t)end;
+        p.tile_off[l + 1] = (int32_t)tiles;
+      }
+      if (l == 0) p.off[0] = p.tile_off[0] = 0;
+    }
+    const uint64_t past = __ballot(l < p.num_reqs && end > i);
+    if (past == 0) return;
+    r = __ffsll((unsigned long long)past) - 1;
+    t = i - (r == 0 ? 0 : (int32_t)__shfl((int)end, r - 1));
+  } else {
+    if (i >= p.off[p.num_reqs]) return;
+    r = find(p.off, p.num_reqs, i);
+    t = i - p.off[r];
+  }
   const int32_t b = p.block_table[(int64_t)r * p.max_pages + (t >> p.page_shift)];
   const bool there = b >= 0 && b < p.pool_rows >> p.page_shift;
   u32x4 v = {0u, 0u, 0u, 0u}, rope = {0u, 0u, 0u, 0u};
@@ -130,60 +171,60 @@ __global__ void __launch_bounds__(256) prefill_rows_kernel(PrefillParams p) {
 
 // ----------------------------------------------------------- expansion
 
-// [token][512] x [head][256][512]^T -> [head][token][256], a workgroup of 4
-// waves a tile of 128 tokens x one head's 256 dimensions, a wave 64 x 128 of
-// it; the contraction in 16 chunks of 32.  Chunks go straight into LDS, three
-// resident (one computed, one complete or on its way, one being left), one
-// barrier a chunk; 16-byte pieces of a row are exchanged by bits 2 and 3 of its
-// number, which puts 16 rows' fragments on distinct banks.  Two workgroups a
-// unit.  The grid runs over heads first: an XCD sees every eighth head, whose
-// weights (256 KB) stay in its L2 over the tokens' tiles.
-constexpr int kGemmM = 128, kGemmN = 256, kGemmK = 32;
-constexpr int kGemmThreads = 256;
+// [token][512] x [head][256][512]^T -> [head][token][256], a workgroup of 2 MW
+// waves a tile of 64 MW tokens x one head's 256 dimensions, a wave 64 x 128 of
+// it; the contraction in 8 chunks of 64.  Chunks go straight into LDS, one
+// computed and one on its way, one barrier a chunk; 16-byte pieces of a row are
+// exchanged by bits 1 to 3 of its number, which puts 16 rows' fragments on
+// distinct banks.  The grid runs over heads first: an XCD sees every eighth head,
+// whose weights (256 KB) stay in its L2 over the tokens' tiles.
+constexpr int kGemmN = 256, kGemmK = 64;
 
+template <int MW>
 struct GemmLds {
   union {
     struct {
-      uint8_t a[kGemmM * 64];
-      uint8_t w[kGemmN * 64];
-    } chunk[3];
-    uint16_t out[kGemmM][kGemmN + 8];
+      uint8_t a[64 * MW * 2 * kGemmK];
+      uint8_t w[kGemmN * 2 * kGemmK];
+    } chunk[2];
+    uint16_t out[64 * MW][kGemmN + 8];
   };
 };
 
 __device__ __forceinline__ int gemm_slot(int row, int piece) {
-  return row * 64 + 16 * (piece ^ ((row >> 2) & 3));
+  return row * 128 + 16 * (piece ^ ((row >> 1) & 7));
 }
 
-// 16-byte pieces of `rows` rows of 32 values, from src rows row_bytes apart.
-template <int ROWS>
+// 16-byte pieces of ROWS rows of 64 values, from src rows row_bytes apart.
+template <int ROWS, int T>
 __device__ __forceinline__ void gemm_fetch(const uint8_t* src, int64_t row_bytes, int32_t last,
                                            uint8_t* dst) {
   const int tid = threadIdx.x, first = __builtin_amdgcn_readfirstlane(tid);
 #pragma unroll
-  for (int i = 0; i < ROWS * 4 / kGemmThreads; ++i) {
-    const int q = tid + kGemmThreads * i, row = q >> 2;
-    const int piece = (q & 3) ^ ((row >> 2) & 3);
-    load_to_lds(src + (int64_t)min(row, last) * row_bytes + 16 * piece,
-                dst + 16 * (first + kGemmThreads * i));
+  for (int i = 0; i < ROWS * 8 / T; ++i) {
+    const int q = tid + T * i, row = q >> 3;
+    const int piece = (q & 7) ^ ((row >> 1) & 7);
+    load_to_lds(src + (int64_t)min(row, last) * row_bytes + 16 * piece, dst + 16 * (first + T * i));
   }
 }
 
-__global__ void __launch_bounds__(kGemmThreads, 2) prefill_expand_kernel(PrefillParams p) {
+template <int MW>
+__global__ void __launch_bounds__(128 * MW, 2) prefill_expand_kernel(PrefillParams p) {
+  constexpr int T = 128 * MW, kGemmM = 64 * MW;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
-  GemmLds& s = *reinterpret_cast<GemmLds*>(lds_raw);
+  GemmLds<MW>& s = *reinterpret_cast<GemmLds<MW>*>(lds_raw);
   const int head = blockIdx.x;
   const int32_t m0 = (int32_t)blockIdx.y * kGemmM;
   const int32_t total = p.off[p.num_reqs];
   if (m0 >= total) return;
   const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, col = l & 31, hi = l >> 5;
-  const int wm = (w & 1) * 64, wn = (w >> 1) * 128;
+  const int wm = (w % MW) * 64, wn = (w / MW) * 128;
   const uint8_t* a = reinterpret_cast<const uint8_t*>(p.lat + (int64_t)m0 * 512);
   const uint8_t* b = reinterpret_cast<const uint8_t*>(p.w + (int64_t)head * kGemmN * 512);
   const int32_t last = min(kGemmM, total - m0) - 1;
   auto fetch = [&](int c) {
-    gemm_fetch<kGemmM>(a + c * 64, 1024, last, s.chunk[c % 3].a);
-    gemm_fetch<kGemmN>(b + c * 64, 1024, kGemmN - 1, s.chunk[c % 3].w);
+    gemm_fetch<kGemmM, T>(a + c * 128, 1024, last, s.chunk[c & 1].a);
+    gemm_fetch<kGemmN, T>(b + c * 128, 1024, kGemmN - 1, s.chunk[c & 1].w);
   };
   f32x16 acc[2][4];
 #pragma unroll
@@ -193,19 +234,15 @@ __global__ void __launch_bounds__(kGemmThreads, 2) prefill_expand_kernel(Prefill
 #pragma unroll
       for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.f;
   fetch(0);
-  fetch(1);
+#pragma unroll 2
   for (int c = 0; c < 512 / kGemmK; ++c) {
-    // chunk c is complete: all but the last fetched one
-    if (c + 1 < 512 / kGemmK)
-      asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
-    else
-      wait_rows();
-    __syncthreads();
-    if (c + 2 < 512 / kGemmK) fetch(c + 2);
-    const uint8_t* ca = s.chunk[c % 3].a;
-    const uint8_t* cw = s.chunk[c % 3].w;
+    wait_rows();
+    lds_barrier();                             // chunk c is complete, chunk c - 1 left
+    if (c + 1 < 512 / kGemmK) fetch(c + 1);
+    const uint8_t* ca = s.chunk[c & 1].a;
+    const uint8_t* cw = s.chunk[c & 1].w;
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
+    for (int ks = 0; ks < 4; ++ks) {
       bf16x8 fa[2], fb[4];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -234,7 +271,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2) prefill_expand_kernel(Prefill
                   bf16_pair(acc[i][j][4 * k + 2], acc[i][j][4 * k + 3])};
   __syncthreads();
   uint16_t* out = p.heads_kv + ((int64_t)head * p.num_kv + m0) * kHeadRow;
-  for (int q = tid; q < kGemmM * 32; q += kGemmThreads) {
+  for (int q = tid; q < kGemmM * 32; q += T) {
     const int row = q >> 5, pc = q & 31;
     if (row <= last)
       *reinterpret_cast<u32x4*>(out + (int64_t)row * kHeadRow + 8 * pc) =
@@ -245,7 +282,8 @@ __global__ void __launch_bounds__(kGemmThreads, 2) prefill_expand_kernel(Prefill
 // ----------------------------------------------------------- attention
 
 // A workgroup of NW waves takes 32 NW queries of one request and head, a wave
-// 32; keys in tiles of 64, two resident in LDS, the next on its way while one
+// 32, and one of `splits` shares of the keys that they see (more than one where
+// the tiles and heads alone leave the chip idle); keys in tiles of 64, two resident in LDS, the next on its way while one
 // is computed; one barrier a tile.  S^T (64 keys x 32 queries) is 24 MFMAs
 // 32x32x16 a wave, O^T (128 x 32) += V^T P^T 16; the probabilities are the B
 // operand from registers, V^T comes through the transposing LDS read.
@@ -286,7 +324,8 @@ __global__ void __launch_bounds__(64 * NW, 2) prefill_attend_kernel(PrefillParam
   TileLds* s = reinterpret_cast<TileLds*>(lds_raw);
   const int head = blockIdx.x;
   const int32_t tiles_all = p.tile_off[p.num_reqs];
-  const int32_t ti = tiles_all - 1 - (int32_t)blockIdx.y;
+  const int32_t split = (int32_t)(blockIdx.y % p.splits);
+  const int32_t ti = tiles_all - 1 - (int32_t)(blockIdx.y / p.splits);
   if (ti < 0) return;
   const int32_t r = find(p.tile_off, p.num_reqs, ti);
   const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, col = l & 31, hi = l >> 5;
@@ -320,16 +359,26 @@ __global__ void __launch_bounds__(64 * NW, 2) prefill_attend_kernel(PrefillParam
       reinterpret_cast<const uint8_t*>(p.heads_kv + ((int64_t)head * p.num_kv + at) * kHeadRow);
   const uint8_t* rope = reinterpret_cast<const uint8_t*>(p.rope + at * kRopeDim);
   const uint8_t* flags = p.flags + at;
-  const int32_t count = (keys + kTile - 1) / kTile;
-  if (count > 0) fetch_tile<NW>(p, hkv, rope, 0, n, s[0]);
-  for (int32_t j = 0; j < count; ++j) {
+  // this split's tiles: [lo, count)
+  const int32_t all = (keys + kTile - 1) / kTile, per = (all + p.splits - 1) / p.splits;
+  const int32_t lo = min(all, split * per), count = min(all, lo + per);
+  auto flag_of = [&](int32_t k) { return k < n ? flags[k] : (uint8_t)1; };
+  uint8_t next_flag = 1;
+  if (count > lo) {
+    next_flag = flag_of(lo * kTile + l);
+    fetch_tile<NW>(p, hkv, rope, lo * kTile, n, s[lo & 1]);
+  }
+  for (int32_t j = lo; j < count; ++j) {
     const int32_t k0 = j * kTile;
     wait_rows();
-    __syncthreads();                           // tile j is complete, tile j - 1 left
-    if (j + 1 < count) fetch_tile<NW>(p, hkv, rope, k0 + kTile, n, s[(j + 1) & 1]);
+    lds_barrier();                             // tile j is complete, tile j - 1 left
+    const uint8_t flag = next_flag;
+    if (j + 1 < count) {
+      next_flag = flag_of(k0 + kTile + l);     // (before the tile: waiting for it waits for no row)
+      fetch_tile<NW>(p, hkv, rope, k0 + kTile, n, s[(j + 1) & 1]);
+    }
     if (k0 >= mine) continue;                  // the wave's queries see nothing here
     const TileLds& t = s[j & 1];
-    const uint8_t flag = k0 + l < n ? flags[k0 + l] : 1;
     f32x16 sc[2];
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
@@ -412,14 +461,74 @@ __global__ void __launch_bounds__(64 * NW, 2) prefill_attend_kernel(PrefillParam
   if (wq + col >= nq) return;
   l_run += __shfl_xor(l_run, 32);
   const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-  uint16_t* out = p.out + (qrow * p.heads + head) * kVal + 4 * hi;
+  const int64_t row = qrow * p.heads + head;
+  if (p.splits == 1) {
+    uint16_t* out = p.out + row * kVal + 4 * hi;
+#pragma unroll
+    for (int dt = 0; dt < 4; ++dt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<u32x2*>(out + 32 * dt + 8 * i) =
+            u32x2{bf16_pair(o[dt][4 * i] * inv, o[dt][4 * i + 1] * inv),
+                  bf16_pair(o[dt][4 * i + 2] * inv, o[dt][4 * i + 3] * inv)};
+    return;
+  }
+  const int64_t ps = (int64_t)split * p.num_q * p.heads + row;
+  if (hi == 0) {
+    p.part_ml[2 * ps] = m_run;
+    p.part_ml[2 * ps + 1] = l_run;
+  }
+  if (l_run == 0.f) return;                    // the merge does not read it
+  uint16_t* po = p.part_o + ps * kVal + 4 * hi;
 #pragma unroll
   for (int dt = 0; dt < 4; ++dt)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<u32x2*>(out + 32 * dt + 8 * i) =
-          u32x2{bf16_pair(o[dt][4 * i] * inv, o[dt][4 * i + 1] * inv),
-                bf16_pair(o[dt][4 * i + 2] * inv, o[dt][4 * i + 3] * inv)};
+      *reinterpret_cast<f16x4*>(po + 32 * dt + 8 * i) =
+          f16x4{(_Float16)(o[dt][4 * i] * inv), (_Float16)(o[dt][4 * i + 1] * inv),
+                (_Float16)(o[dt][4 * i + 2] * inv), (_Float16)(o[dt][4 * i + 3] * inv)};
+}
+
+// Merges the key splits of a (query, head), 16 lanes 8 dimensions each: with
+// w_s = 2^(m_s - M) l_s, out = sum_s w_s out_s / sum_s w_s.
+__global__ void __launch_bounds__(256) prefill_merge_kernel(PrefillParams p) {
+  const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4), rows = (int64_t)p.num_q * p.heads;
+  if (row >= rows) return;
+  const int32_t q = (int32_t)(row / p.heads);
+  // a query of no request: not written, left as it was
+  if (q < p.query_start(0) || q >= p.query_start(p.num_reqs)) return;
+  const int c = threadIdx.x & 15;
+  float M = -INFINITY;
+  for (int sp = 0; sp < p.splits; ++sp) {
+    const int64_t ps = (int64_t)sp * rows + row;
+    if (p.part_ml[2 * ps + 1] != 0.f) M = fmaxf(M, p.part_ml[2 * ps]);
+  }
+  float sum = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int sp = 0; sp < p.splits; ++sp) {
+    const int64_t ps = (int64_t)sp * rows + row;
+    const float l = p.part_ml[2 * ps + 1];
+    if (l == 0.f) continue;                    // nothing seen there: not written
+    const float x = exp2f(p.part_ml[2 * ps] - M) * l;          // NaN stays NaN
+    sum += x;
+    const f16x8 h = *reinterpret_cast<const f16x8*>(p.part_o + ps * kVal + 8 * c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] += x * (float)h[i];
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  *reinterpret_cast<u32x4*>(p.out + row * kVal + 8 * c) =
+      u32x4{bf16_pair(acc[0] * inv, acc[1] * inv), bf16_pair(acc[2] * inv, acc[3] * inv),
+            bf16_pair(acc[4] * inv, acc[5] * inv), bf16_pair(acc[6] * inv, acc[7] * inv)};
+}
+
+template <int MW>
+hipError_t launch_expand(const PrefillParams& p, hipStream_t stream) {
+  static std::atomic<uint64_t> raised{0};
+  const auto fn = prefill_expand_kernel<MW>;
+  const hipError_t e = allow_full_lds(reinterpret_cast<const void*>(fn), raised);
+  if (e != hipSuccess) return e;
+  return launch_kernel(fn,
+                       dim3((uint32_t)p.heads, (uint32_t)((p.num_kv + 64 * MW - 1) / (64 * MW))),
+                       dim3(128 * MW), sizeof(GemmLds<MW>), stream, p);
 }
 
 constexpr size_t kAlign = 256;
@@ -428,9 +537,26 @@ size_t up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 }  // namespace
 
 size_t plan_prefill(PrefillParams& p, void* workspace) {
-  // 8 waves a tile where the queries fill it
-  p.tile_rows = p.num_q >= 256 * (int64_t)p.num_reqs ? 256 : 128;
-  p.max_tiles = (int32_t)min((int64_t)INT32_MAX, (int64_t)p.num_q / p.tile_rows + p.num_reqs);
+  // Tiles of 256 queries (8 waves, one workgroup a unit) where the queries fill
+  // them and the chip, else of 128 (4 waves, two a unit); then as many key splits
+  // as give the fewest key-tile times (about 1.4 us, 2 for 4 waves) over the
+  // rounds of the chip, a workgroup's start and end and the merge counted in them
+  const int64_t R = p.num_reqs > 0 ? p.num_reqs : 1, nq = p.num_q;
+  p.tile_rows = nq >= 256 * R && (nq / 256 + R) * p.heads >= 256 ? 256 : 128;
+  p.max_tiles = (int32_t)min((int64_t)INT32_MAX, nq / p.tile_rows + p.num_reqs);
+  const int64_t slots = p.tile_rows == 256 ? 256 : 512;
+  const int64_t base = (nq + p.tile_rows - 1) / p.tile_rows * p.heads;
+  const int64_t tiles = (p.num_kv / R + kTile - 1) / kTile;
+  p.splits = 1;
+  double best = 1e300;
+  for (int n = 1; n <= kPrefillMaxSplits && n <= (tiles > 1 ? tiles : 1); n *= 2) {
+    const double t = (double)((base * n + slots - 1) / slots) * ((tiles + n - 1) / n + 3) +
+                     (n > 1 ? 3 + (double)nq * p.heads * n / 10000 : 0.0);
+    if (t < best) {
+      best = t;
+      p.splits = n;
+    }
+  }
   uint8_t* at = static_cast<uint8_t*>(workspace);
   size_t n = 0;
   auto take = [&](size_t bytes) {
@@ -438,34 +564,40 @@ size_t plan_prefill(PrefillParams& p, void* workspace) {
     n += up(bytes);
     return q;
   };
-  const size_t R = p.num_reqs, kv = p.num_kv, H = p.heads;
-  p.off = reinterpret_cast<int32_t*>(take((R + 1) * 4));
-  p.tile_off = reinterpret_cast<int32_t*>(take((R + 1) * 4));
+  const size_t kv = p.num_kv, H = p.heads;
+  p.off = reinterpret_cast<int32_t*>(take((p.num_reqs + (size_t)1) * 4));
+  p.tile_off = reinterpret_cast<int32_t*>(take((p.num_reqs + (size_t)1) * 4));
   p.flags = take(kv);
   p.lat = reinterpret_cast<uint16_t*>(take(kv * 512 * 2));
   p.rope = reinterpret_cast<uint16_t*>(take(kv * kRopeDim * 2));
   p.heads_kv = reinterpret_cast<uint16_t*>(take(H * kv * kHeadRow * 2));
+  if (p.splits > 1) {
+    p.part_o = reinterpret_cast<uint16_t*>(take((size_t)p.splits * nq * H * kVal * 2));
+    p.part_ml = reinterpret_cast<float*>(take((size_t)p.splits * nq * H * 2 * 4));
+  }
   return n;
 }
 
 bool prefill_fits(const PrefillParams& p) {
-  return p.max_tiles <= 65535 && (p.num_kv + kGemmM - 1) / kGemmM <= 65535;
+  return (int64_t)p.max_tiles * p.splits <= 65535 && (p.num_kv + 127) / 128 <= 65535;
 }
 
 hipError_t launch_prefill(const PrefillParams& p, bool fp4, hipStream_t stream) {
   if (p.num_reqs == 0 || p.num_q == 0) return hipSuccess;
-  hipError_t e = launch_kernel(prefill_plan_kernel, dim3(1), dim3(1024), 0, stream, p);
-  if (e != hipSuccess) return e;
-  if (p.num_kv > 0) {
+  hipError_t e = hipSuccess;
+  if (p.num_reqs > kInlineReqs) {
+    e = launch_kernel(prefill_plan_kernel, dim3(1), dim3(1024), 0, stream, p);
+    if (e != hipSuccess) return e;
+  }
+  // (at least one workgroup: the offsets)
+  {
     e = launch_kernel(fp4 ? prefill_rows_kernel<true> : prefill_rows_kernel<false>,
-                      dim3((uint32_t)((p.num_kv + 3) / 4)), dim3(256), 0, stream, p);
+                      dim3((uint32_t)((p.num_kv + 3) / 4 > 0 ? (p.num_kv + 3) / 4 : 1)), dim3(256), 0,
+                      stream, p);
     if (e != hipSuccess) return e;
-    static std::atomic<uint64_t> raised{0};
-    e = allow_full_lds(reinterpret_cast<const void*>(prefill_expand_kernel), raised);
-    if (e != hipSuccess) return e;
-    e = launch_kernel(prefill_expand_kernel,
-                      dim3((uint32_t)p.heads, (uint32_t)((p.num_kv + kGemmM - 1) / kGemmM)),
-                      dim3(kGemmThreads), sizeof(GemmLds), stream, p);
+  }
+  if (p.num_kv > 0) {
+    e = p.num_kv >= 1024 ? launch_expand<4>(p, stream) : launch_expand<2>(p, stream);
     if (e != hipSuccess) return e;
   }
   static std::atomic<uint64_t> raised[2];
@@ -473,8 +605,12 @@ hipError_t launch_prefill(const PrefillParams& p, bool fp4, hipStream_t stream) 
   auto fn = big ? prefill_attend_kernel<8> : prefill_attend_kernel<4>;
   e = allow_full_lds(reinterpret_cast<const void*>(fn), raised[big]);
   if (e != hipSuccess) return e;
-  return launch_kernel(fn, dim3((uint32_t)p.heads, (uint32_t)p.max_tiles),
-                       dim3((uint32_t)p.tile_rows * 2), 2 * sizeof(TileLds), stream, p);
+  e = launch_kernel(fn, dim3((uint32_t)p.heads, (uint32_t)(p.max_tiles * p.splits)),
+                    dim3((uint32_t)p.tile_rows * 2), 2 * sizeof(TileLds), stream, p);
+  if (e != hipSuccess || p.splits == 1) return e;
+  const int64_t rows = (int64_t)p.num_q * p.heads;
+  return launch_kernel(prefill_merge_kernel, dim3((uint32_t)((rows + 15) / 16)), dim3(256), 0, stream,
+                       p);
 }
 
 }  // namespace hs
