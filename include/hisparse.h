@@ -459,8 +459,8 @@ typedef struct {
  * ones mix).  Uses batch->num_reqs, max_pages, block_table and kv_pool only.
  * Errors: HS_ERR_INVALID_ARGUMENT (null or misaligned pointers with work to
  * do, negative sizes, bad strides, a bad layer or layout),
- * HS_ERR_UNSUPPORTED (another row_bytes, over 1,048,576 heads),
- * HS_ERR_LAUNCH.
+ * HS_ERR_UNSUPPORTED (another row_bytes, over 1,048,576 heads, a launch of
+ * 2^32 threads), HS_ERR_LAUNCH.
  */
 hs_status hs_mla_append(const hs_layout* layout, const hs_batch* batch, int32_t layer,
                         const hs_append* tokens, int32_t* row_ids, uint16_t* values,
@@ -483,7 +483,7 @@ hs_status hs_mla_append(const hs_layout* layout, const hs_batch* batch, int32_t 
  * Errors: HS_ERR_INVALID_ARGUMENT (null or misaligned pointers with work to
  * do, a short workspace, num_heads < 1, negative sizes, bad layout),
  * HS_ERR_UNSUPPORTED (another row_bytes, over 1,048,576 tokens, heads or
- * top_k, a launch over 2^31 workgroups), HS_ERR_LAUNCH.
+ * top_k, a launch of 2^32 threads), HS_ERR_LAUNCH.
  */
 hs_status hs_sparse_mla_decode_fp4(const hs_layout* layout, const uint8_t* kv_layer,
                                    const int32_t* row_ids, int32_t num_tokens, int32_t top_k,
@@ -520,7 +520,7 @@ size_t hs_sparse_mla_fp4_workspace_bytes(int32_t num_tokens, int32_t num_heads, 
  * Errors: HS_ERR_INVALID_ARGUMENT (null or misaligned pointers with work to
  * do, a short workspace, num_pos or num_heads < 1, a negative max_ctx, a bad
  * layer or layout), HS_ERR_UNSUPPORTED (another row_bytes, P * H over
- * 1,048,576, a launch over 2^31 workgroups), HS_ERR_LAUNCH.
+ * 1,048,576, a launch of 2^32 threads), HS_ERR_LAUNCH.
  */
 hs_status hs_paged_mla_decode(const hs_layout* layout, const hs_batch* batch, int32_t layer,
                               const uint16_t* q, int32_t num_pos, int32_t num_heads,

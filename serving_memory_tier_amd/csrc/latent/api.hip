@@ -15,6 +15,8 @@ using hs::log2i;
 
 namespace {
 
+constexpr int32_t kMaxRows = 1 << 20;   // heads, query rows an item, tokens, list entries
+
 // Whether the layout's rows are 4-bit ones; HS_ERR_UNSUPPORTED where they are
 // neither format.
 hs_status row_format(const hs_layout* lay, bool* fp4) {
@@ -22,6 +24,8 @@ hs_status row_format(const hs_layout* lay, bool* fp4) {
   *fp4 = lay->row_bytes == HS_ROW_FP4;
   return HS_OK;
 }
+
+bool aligned4(const void* p) { return ((uintptr_t)p & 3) == 0; }
 
 bool bad_stride(int64_t stride, int64_t multiple) { return stride < 0 || stride % multiple != 0; }
 
@@ -42,7 +46,7 @@ hs_status hs_mla_append(const hs_layout* layout, const hs_batch* batch, int32_t 
   if (a.num_tokens < 0 || a.num_heads < 0 || batch->num_reqs < 0 || batch->max_pages < 1 ||
       (a.rope_interleaved != 0 && a.rope_interleaved != 1) || a.reserved != 0)
     return HS_ERR_INVALID_ARGUMENT;
-  if (a.num_heads > (1 << 20)) return HS_ERR_UNSUPPORTED;
+  if (a.num_heads > kMaxRows) return HS_ERR_UNSUPPORTED;
   if (a.num_tokens == 0) return HS_OK;
   if (!a.token_req || !a.positions || !a.latent || !a.rope || !a.rope_freq || !batch->kv_pool ||
       (batch->num_reqs > 0 && !batch->block_table))
@@ -79,23 +83,23 @@ hs_status hs_mla_append(const hs_layout* layout, const hs_batch* batch, int32_t 
   p.q_out_head_stride = a.q_out_head_stride;
   p.row_ids = row_ids;
   p.values = values;
+  if (!hs::append_fits(p)) return HS_ERR_UNSUPPORTED;
   return from_hip(hs::launch_append(p, fp4, a.rope_interleaved == 1, stream), "append launch");
 }
 
 namespace {
-
-constexpr int32_t kMaxRows = 1 << 20;   // query rows an item, tokens, list entries
 
 // Checks the workspace and the outputs of an absorbed attention call and
 // enqueues it.
 hs_status attend(hs::DecodeParams p, bool fp4, bool paged, int64_t keys, const void* out,
                  const void* lse, void* workspace, size_t workspace_bytes, const char* what,
                  hipStream_t stream) {
-  if (!p.q || !out || !lse || !aligned16(p.q) || !aligned16(out)) return HS_ERR_INVALID_ARGUMENT;
+  if (!p.q || !out || !lse || !aligned16(p.q) || !aligned16(out) || !aligned4(lse))
+    return HS_ERR_INVALID_ARGUMENT;
   const size_t need = hs::plan_decode(p, keys);
+  if (!hs::decode_fits(p)) return HS_ERR_UNSUPPORTED;
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
     return HS_ERR_INVALID_ARGUMENT;
-  if (!hs::decode_fits(p)) return HS_ERR_UNSUPPORTED;
   return from_hip(hs::launch_decode(p, fp4, paged, workspace, stream), what);
 }
 
@@ -201,7 +205,8 @@ hs_status hs_mla_prefill(const hs_layout* layout, const hs_batch* batch, int32_t
   if (batch->num_reqs == 0 || num_q == 0) return HS_OK;
   if (!q_start || !q || !w_kv || !out || !batch->kv_pool || !batch->block_table || !batch->ctx_len)
     return HS_ERR_INVALID_ARGUMENT;
-  if (!aligned16(batch->kv_pool) || !aligned16(q) || !aligned16(w_kv) || !aligned16(out))
+  if (!aligned16(batch->kv_pool) || !aligned16(q) || !aligned16(w_kv) || !aligned16(out) ||
+      !aligned4(q_start))
     return HS_ERR_INVALID_ARGUMENT;
   hs::PrefillParams p{};
   p.kv = batch->kv_pool + (int64_t)layer * layout->pool_layer_stride;
@@ -220,8 +225,8 @@ hs_status hs_mla_prefill(const hs_layout* layout, const hs_batch* batch, int32_t
   p.scale = sm_scale;
   p.out = out;
   const size_t need = hs::plan_prefill(p, workspace);
-  if (!workspace || workspace_bytes < need || !aligned16(workspace)) return HS_ERR_INVALID_ARGUMENT;
   if (!hs::prefill_fits(p)) return HS_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < need || !aligned16(workspace)) return HS_ERR_INVALID_ARGUMENT;
   return from_hip(hs::launch_prefill(p, fp4, stream), "MLA prefill launch");
 }
 

@@ -228,12 +228,15 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p) {
 
 }  // namespace
 
+bool append_fits(const AppendParams& p) {
+  return grid_fits(p.num_tokens, kThreads) && p.num_heads <= 65535 * kHeadsPerRound * kRounds;
+}
+
 hipError_t launch_append(AppendParams p, bool fp4, bool interleaved, hipStream_t stream) {
   if (p.num_tokens == 0) return hipSuccess;
   p.heads_per_group = kHeadsPerRound * kRounds;
-  const int64_t gy = p.num_heads > 0
+  const int32_t gy = p.num_heads > 0
                          ? (p.num_heads + p.heads_per_group - 1) / p.heads_per_group : 1;
-  if (gy > 65535) return hipErrorInvalidValue;
   const dim3 grid((uint32_t)p.num_tokens, (uint32_t)gy);
   auto fn = fp4 ? (interleaved ? append_kernel<true, true> : append_kernel<true, false>)
                 : (interleaved ? append_kernel<false, true> : append_kernel<false, false>);

@@ -686,7 +686,7 @@ size_t plan_decode(DecodeParams& p, int64_t keys) {
 }
 
 bool decode_fits(const DecodeParams& p) {
-  return decode_grid(p) <= INT32_MAX && (int64_t)p.items * p.rows <= 4 * (int64_t)INT32_MAX;
+  return grid_fits(decode_grid(p), 512) && grid_fits(((int64_t)p.items * p.rows + 3) / 4, 256);
 }
 
 hipError_t launch_decode(DecodeParams p, bool fp4, bool paged, void* workspace,

@@ -10,6 +10,12 @@ namespace hs {
 constexpr int kFp8RowBytes = 656;  // 512 E4M3, 4 float32 scales, 64 bfloat16
 constexpr int kFp4RowBytes = 400;  // 512 E2M1 (two a byte), 16 E8M0 scales, 64 bfloat16
 
+// Whether a launch of so many workgroups of so many threads is one that the
+// device takes: a grid dimension holds less than 2^32 threads.
+inline bool grid_fits(int64_t groups, int threads) {
+  return groups >= 0 && groups <= (int64_t)(UINT32_MAX / (uint32_t)threads);
+}
+
 // Rows written at their positions, with the rotation (append.hip).
 struct AppendParams {
   uint8_t* pool;            // one layer
@@ -33,6 +39,8 @@ struct AppendParams {
   int32_t heads_per_group;  // set by launch_append
 };
 
+// Whether the launch's grid is within the device's limits.
+bool append_fits(const AppendParams& p);
 hipError_t launch_append(AppendParams p, bool fp4, bool interleaved, hipStream_t stream);
 
 // Absorbed latent attention (decode.hip): M query rows an item, 576 wide, over

@@ -115,3 +115,159 @@ def test_append_binding_refuses_wrong_tensors():
         hs.append_of(**args(token_req=t(2, dtype=torch.int64)))
     with pytest.raises(ValueError, match="current CUDA device"):
         hs.append_of(**args())              # host tensors
+
+
+def test_append_too_many_tokens(lib):
+    r = ctypes.byref
+    assert lib.hs_mla_append(r(layout()), r(batch()), 0, r(append(num_tokens=2 ** 31 - 1)), FAKE,
+                             FAKE, None) == 2
+
+
+BIG = 1 << 40      # a workspace's stated size
+
+
+@pytest.mark.parametrize("lay,kw,code", [
+    (dict(page_size=48), {}, 1), ({}, {}, 2), (dict(row_bytes=656), {}, 2),
+    (dict(row_bytes=416), {}, 2),
+] + [(dict(row_bytes=400), kw, code) for kw, code in [
+    (dict(tokens=-1), 1), (dict(k=-1), 1), (dict(heads=0), 1), (dict(heads=-3), 1),
+    (dict(tokens=(1 << 20) + 1), 2), (dict(k=(1 << 20) + 1), 2), (dict(heads=(1 << 20) + 1), 2),
+    (dict(kv=None), 1), (dict(kv=0x1008), 1), (dict(ids=None), 1), (dict(q=None), 1),
+    (dict(q=0x1008), 1), (dict(out=None), 1), (dict(out=0x1002), 1), (dict(lse=None), 1),
+    (dict(lse=0x1002), 1), (dict(ws=None), 1), (dict(ws=0x1008), 1), (dict(size=0), 1),
+    (dict(size="short"), 1), (dict(tokens=1 << 20, heads=1 << 20), 2), (dict(tokens=0), 0),
+    (dict(tokens=0, kv=None, ids=None, q=None, out=None, lse=None, ws=None), 0),
+]])
+def test_sparse_refusals(lib, lay, kw, code):
+    a = dict(kv=FAKE, ids=FAKE, tokens=2, k=5000, q=FAKE, heads=16, out=FAKE, lse=FAKE, ws=FAKE,
+             size=BIG)
+    a.update(kw)
+    need = lib.hs_sparse_mla_fp4_workspace_bytes(a["tokens"], a["heads"], a["k"])
+    if a["size"] == "short":
+        a["size"] = need - 1
+    l = layout(**lay)
+    assert lib.hs_sparse_mla_decode_fp4(ctypes.byref(l), a["kv"], a["ids"], a["tokens"], a["k"],
+                                        a["q"], a["heads"], 1.0, a["out"], a["lse"], a["ws"],
+                                        a["size"], None) == code
+    assert lib.hs_sparse_mla_decode_fp4(None, FAKE, FAKE, 1, 1, FAKE, 1, 1.0, FAKE, FAKE, None, 0,
+                                        None) == 1
+
+
+@pytest.mark.parametrize("lay,bat,kw,code", [
+    (dict(page_size=0), {}, {}, 1), (dict(row_bytes=640), {}, {}, 2),
+    ({}, {}, dict(layer=-1), 1), ({}, {}, dict(layer=2), 1),
+    ({}, dict(num_reqs=-1), {}, 1), ({}, dict(max_pages=0), {}, 1), ({}, dict(kv_pool=None), {}, 1),
+    ({}, dict(kv_pool=0x1008), {}, 1), ({}, dict(block_table=None), {}, 1),
+    ({}, dict(ctx_len=None), {}, 1), ({}, {}, dict(pos=0), 1), ({}, {}, dict(heads=0), 1),
+    ({}, {}, dict(ctx=-1), 1), ({}, {}, dict(pos=1 << 11, heads=1 << 10), 2),
+    ({}, {}, dict(pos=2 ** 31 - 1, heads=2 ** 31 - 1), 2),
+    ({}, {}, dict(q=None), 1), ({}, {}, dict(q=0x1008), 1), ({}, {}, dict(out=None), 1),
+    ({}, {}, dict(out=0x1008), 1), ({}, {}, dict(lse=None), 1), ({}, {}, dict(lse=0x1001), 1),
+    ({}, {}, dict(ws=None), 1),
+    ({}, {}, dict(ws=0x1008), 1), ({}, {}, dict(size="short"), 1),
+    ({}, dict(num_reqs=2 ** 31 - 1), dict(size=1 << 62), 2),
+    ({}, dict(num_reqs=0), dict(q=None, out=None, ws=None), 0),
+])
+def test_paged_refusals(lib, lay, bat, kw, code):
+    a = dict(layer=1, q=FAKE, pos=1, heads=16, ctx=5000, out=FAKE, lse=FAKE, ws=FAKE, size=BIG)
+    a.update(kw)
+    l, b = layout(**lay), batch(**{**dict(ctx_len=FAKE), **bat})
+    if a["size"] == "short":
+        a["size"] = lib.hs_paged_mla_workspace_bytes(b.num_reqs, a["pos"], a["heads"], a["ctx"]) - 1
+    f = lib.hs_paged_mla_decode
+    assert f(ctypes.byref(l), ctypes.byref(b), a["layer"], a["q"], a["pos"], a["heads"], a["ctx"],
+             1.0, a["out"], a["lse"], a["ws"], a["size"], None) == code
+    assert f(ctypes.byref(l), None, 0, FAKE, 1, 1, 1, 1.0, FAKE, FAKE, None, 0, None) == 1
+    assert f(None, ctypes.byref(b), 0, FAKE, 1, 1, 1, 1.0, FAKE, FAKE, None, 0, None) == 1
+
+
+@pytest.mark.parametrize("lay,bat,kw,code", [
+    (dict(page_size=0), {}, {}, 1), (dict(row_bytes=640), {}, {}, 2),
+    ({}, {}, dict(layer=-1), 1), ({}, {}, dict(layer=2), 1),
+    ({}, dict(num_reqs=-1), {}, 1), ({}, dict(max_pages=0), {}, 1), ({}, dict(kv_pool=None), {}, 1),
+    ({}, dict(kv_pool=0x1008), {}, 1), ({}, dict(block_table=None), {}, 1),
+    ({}, dict(ctx_len=None), {}, 1), ({}, {}, dict(start=None), 1), ({}, {}, dict(num_q=-1), 1),
+    ({}, {}, dict(start=0x1002), 1),
+    ({}, {}, dict(num_kv=-1), 1), ({}, {}, dict(heads=0), 1), ({}, {}, dict(heads=(1 << 20) + 1), 2),
+    ({}, dict(num_reqs=(1 << 20) + 1), {}, 2), ({}, {}, dict(q=None), 1), ({}, {}, dict(q=0x1008), 1),
+    ({}, {}, dict(w=None), 1), ({}, {}, dict(w=0x1008), 1), ({}, {}, dict(out=None), 1),
+    ({}, {}, dict(out=0x1008), 1), ({}, {}, dict(ws=None), 1), ({}, {}, dict(ws=0x1008), 1),
+    ({}, {}, dict(size="short"), 1), ({}, {}, dict(num_q=2 ** 31 - 1, size=1 << 62), 2),
+    ({}, {}, dict(num_kv=2 ** 31 - 1, size=1 << 62), 2),
+    ({}, {}, dict(num_kv=65535 * 128 + 1, size=1 << 62), 2),
+    ({}, {}, dict(num_q=0, q=None, out=None, ws=None), 0),
+    ({}, dict(num_reqs=0), dict(q=None, out=None, ws=None), 0),
+])
+def test_prefill_refusals(lib, lay, bat, kw, code):
+    a = dict(layer=0, start=FAKE, num_q=100, num_kv=300, q=FAKE, heads=4, w=FAKE, out=FAKE, ws=FAKE,
+             size=BIG)
+    a.update(kw)
+    l, b = layout(**lay), batch(**{**dict(ctx_len=FAKE), **bat})
+    if a["size"] == "short":
+        a["size"] = lib.hs_mla_prefill_workspace_bytes(b.num_reqs, a["num_q"], a["num_kv"],
+                                                       a["heads"]) - 1
+    f = lib.hs_mla_prefill
+    assert f(ctypes.byref(l), ctypes.byref(b), a["layer"], a["start"], a["num_q"], a["num_kv"],
+             a["q"], a["heads"], a["w"], 1.0, a["out"], a["ws"], a["size"], None) == code
+    assert f(ctypes.byref(l), None, 0, FAKE, 1, 1, FAKE, 1, FAKE, 1.0, FAKE, FAKE, BIG, None) == 1
+    assert f(None, ctypes.byref(b), 0, FAKE, 1, 1, FAKE, 1, FAKE, 1.0, FAKE, FAKE, BIG, None) == 1
+
+
+def test_workspace_sizes(lib):
+    assert hs.hs_sparse_mla_fp4_workspace_bytes(0, 16, 100) == 0
+    assert hs.hs_sparse_mla_fp4_workspace_bytes(4, 16, -1) == 0
+    assert hs.hs_paged_mla_workspace_bytes(4, 0, 16, 100) == 0
+    assert hs.hs_paged_mla_workspace_bytes(4, 1, 16, -1) == 0
+    assert hs.hs_mla_prefill_workspace_bytes(1, 0, 100, 4) == 0
+    assert hs.hs_mla_prefill_workspace_bytes(1, 10, -1, 4) == 0
+    # a split's row: 512 halves and two floats
+    for n, heads, k in ((1, 16, 4096), (32, 128, 2048), (3, 129, 70000)):
+        assert hs.hs_sparse_mla_fp4_workspace_bytes(n, heads, k) % (n * heads * 1032) == 0
+    # the expanded keys and values at least, whatever the requests
+    assert hs.hs_mla_prefill_workspace_bytes(3, 100, 1000, 8) >= 1000 * 8 * 512
+    # sizes beyond 32 bits
+    assert hs.hs_mla_prefill_workspace_bytes(1, 4096, 1 << 17, 128) > 1 << 33
+
+
+def test_bindings_refuse_wrong_tensors():
+    t = torch.zeros
+    i32, bf, f32, u8 = torch.int32, torch.bfloat16, torch.float32, torch.uint8
+    lay = layout(row_bytes=400)
+    sparse = lambda **kw: hs.hs_sparse_mla_decode_fp4(lay, **{**dict(
+        kv_layer=t(64, 400, dtype=u8), row_ids=t(2, 8, dtype=i32), num_tokens=2, top_k=8,
+        q=t(2, 4, 576, dtype=bf), num_heads=4, sm_scale=1.0, out=t(2, 4, 512, dtype=bf),
+        lse=t(2, 4)), **kw})
+    with pytest.raises(ValueError, match="row_ids"):
+        sparse(row_ids=t(2, 7, dtype=i32))
+    with pytest.raises(ValueError, match="q has"):
+        sparse(q=t(2, 4, 512, dtype=bf))
+    with pytest.raises(TypeError, match="kv_layer"):
+        sparse(kv_layer=t(64, 400, dtype=i32))
+    with pytest.raises(ValueError, match="current CUDA device"):
+        sparse()
+    with pytest.raises(TypeError, match="cannot pass"):
+        sparse(kv_layer=[1])
+    b = batch(ctx_len=FAKE)
+    paged = lambda **kw: hs.hs_paged_mla_decode(lay, b, 0, **{**dict(
+        q=FAKE, num_pos=1, num_heads=4, max_ctx=9, sm_scale=1.0, out=FAKE, lse=FAKE), **kw})
+    with pytest.raises(ValueError, match="out has"):
+        paged(out=t(2, 4, 576, dtype=bf))
+    with pytest.raises(TypeError, match="lse"):
+        paged(lse=t(2, 4, dtype=bf))
+    with pytest.raises(ValueError, match="lse has"):
+        paged(lse=t(3, 4))
+    with pytest.raises(TypeError, match="out is"):
+        paged(out=t(2, 4, 512, dtype=f32))
+    prefill = lambda **kw: hs.hs_mla_prefill(lay, b, 0, **{**dict(
+        q_start=FAKE, num_q=5, num_kv=9, q=FAKE, num_heads=4, w_kv=FAKE, sm_scale=1.0, out=FAKE,
+        workspace=None), **kw})
+    with pytest.raises(ValueError, match="q_start"):
+        prefill(q_start=t(2, dtype=i32))
+    with pytest.raises(TypeError, match="q_start"):
+        prefill(q_start=t(3, dtype=torch.int64))
+    with pytest.raises(ValueError, match="w_kv"):
+        prefill(w_kv=t(4, 256, 576, dtype=bf))
+    with pytest.raises(ValueError, match="current CUDA device"):
+        prefill(workspace=t(64, dtype=u8))
+    with pytest.raises(hs.HsError):
+        prefill(stream=0)
