@@ -269,6 +269,13 @@ __global__ void __launch_bounds__(128 * NP) decode_fp4_kernel(DecodeParams p) {
   Lds4<NP>& s = *reinterpret_cast<Lds4<NP>*>(lds_raw);
   Share sh;
   if (!begin<PAGED, 32 * NP>(p, s.lists, sh)) return;       // the whole workgroup
+  int32_t* ids = s.lists.ids;
+  const int blocks = (sh.n + kKeys - 1) / kKeys;
+  Fetch4<T> f;
+  if (blocks > 0) {                            // before the queries: waited for first
+    f.load_ids(ids);
+    f.load(p.kv);
+  }
   bf16x8 qb[kQueryRegs];
   {
     // a lane past the last row takes row 0's queries; it writes nothing
@@ -293,12 +300,7 @@ __global__ void __launch_bounds__(128 * NP) decode_fp4_kernel(DecodeParams p) {
     for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
   float m_run = -INFINITY, l_run = 0.f;        // l_run: this lane's keys only
   const float qk_scale = p.scale * kLog2e;
-  int32_t* ids = s.lists.ids;
-  const int blocks = (sh.n + kKeys - 1) / kKeys;
-  Fetch4<T> f;
   if (blocks > 0) {
-    f.load_ids(ids);
-    f.load(p.kv);
     f.store(s.blk[0], ids, PAGED && kKeys > sh.edge, sh.edge);
     if (blocks > 1) {
       f.load_ids(ids + kKeys);
@@ -586,28 +588,35 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(DecodeParams p) {
   if (mrow >= (int64_t)p.items * p.rows) return;
   const int64_t item = mrow / p.rows, m = mrow - item * p.rows;
   const int64_t ps0 = item * p.splits * p.rows + m;
-  float M = -INFINITY;
-  for (int sp = l; sp < p.splits; sp += 64) {
-    const int64_t ps = ps0 + (int64_t)sp * p.rows;
-    if (p.part_ml[2 * ps + 1] != 0.f) M = fmaxf(M, p.part_ml[2 * ps]);
+  // eight splits' outputs at a time, the first ones beside the sums; one that saw
+  // nothing was not written, and has no weight
+  f16x8 h[8];
+  auto read = [&](int sp) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      h[j] = *reinterpret_cast<const f16x8*>(
+          p.part_o + (ps0 + (int64_t)min(sp + j, p.splits - 1) * p.rows) * kLatent + 8 * l);
+  };
+  auto sums = [&](int sp) {
+    return sp < p.splits
+               ? *reinterpret_cast<const f32x2*>(p.part_ml + 2 * (ps0 + (int64_t)sp * p.rows))
+               : f32x2{-INFINITY, 0.f};
+  };
+  f32x2 ml = sums(l);
+  read(0);
+  float M = ml[1] != 0.f ? ml[0] : -INFINITY;
+  for (int sp = l + 64; sp < p.splits; sp += 64) {
+    const f32x2 v = sums(sp);
+    if (v[1] != 0.f) M = fmaxf(M, v[0]);
   }
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) M = fmaxf(M, __shfl_xor(M, d));
   float sum = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int s0 = 0; s0 < p.splits; s0 += 64) {
-    float wgt = 0.f;
-    if (s0 + l < p.splits) {
-      const int64_t ps = ps0 + (int64_t)(s0 + l) * p.rows;
-      const float ls = p.part_ml[2 * ps + 1];
-      if (ls != 0.f) wgt = exp2f(p.part_ml[2 * ps] - M) * ls;     // NaN stays NaN
-    }
-    // eight splits' loads at a time; one that saw nothing was not written
+    if (s0 > 0) ml = sums(s0 + l);
+    const float wgt = ml[1] != 0.f ? exp2f(ml[0] - M) * ml[1] : 0.f;    // NaN stays NaN
     for (int j0 = 0; j0 < min(64, p.splits - s0); j0 += 8) {
-      f16x8 h[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        h[j] = *reinterpret_cast<const f16x8*>(
-            p.part_o + (ps0 + (int64_t)min(s0 + j0 + j, p.splits - 1) * p.rows) * kLatent + 8 * l);
+      if (s0 + j0 > 0) read(s0 + j0);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float x = __shfl(wgt, j0 + j);   // 0 past the last split
@@ -643,9 +652,10 @@ hipError_t launch_wide(const DecodeParams& p, bool fp4, bool paged, hipStream_t 
 
 }  // namespace
 
-// In block times (about 3 us): a workgroup's start and end, a merge's launch, and
-// the rows whose partial outputs (2 KB written and read) take one.
-constexpr int kStartBlocks = 4, kMergeBlocks = 2;
+// In block times (about 2 us): a workgroup's start and end, a merge's launch, the
+// splits that it takes one over, and the rows whose partial outputs (2 KB written
+// and read) take one.
+constexpr int kStartBlocks = 4, kMergeBlocks = 2, kMergeSplits = 12;
 constexpr double kMergeRows = 7000;
 
 int64_t decode_grid(const DecodeParams& p) {
@@ -664,15 +674,18 @@ size_t plan_decode(DecodeParams& p, int64_t keys) {
   const int64_t least = (blocks * kKeys + kDecodeSplitKeys - 1) / kDecodeSplitKeys;
   int64_t best = 1;
   double best_t = 1e300;
-  for (int r = 0; r <= 4; ++r) {               // as many as fill r rounds; 0: as few as may be
-    int64_t n = r > 0 && base > 0 ? r * slots / base : 1;
+  // as few as may be; as many as fill 1 to 4 rounds; a half and a quarter of the blocks
+  for (int r = 0; r <= 6; ++r) {
+    int64_t n = r > 4 ? blocks / (2 * (r - 4)) : r > 0 && base > 0 ? r * slots / base : 1;
     n = n < least ? least : n;
     n = n > blocks ? blocks : n;
     if (n < 1) n = 1;
     const int64_t per = (blocks + n - 1) / n;
     if (per > 0) n = (blocks + per - 1) / per;
     const double t = (double)((base * n + slots - 1) / slots) * (per + kStartBlocks) +
-                     (n > 1 ? kMergeBlocks + (double)p.items * p.rows * n / kMergeRows : 0.0);
+                     (n > 1 ? kMergeBlocks + (double)n / kMergeSplits +
+                                  (double)p.items * p.rows * n / kMergeRows
+                            : 0.0);
     if (t < best_t) {
       best_t = t;
       best = n;
