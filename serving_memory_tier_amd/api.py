@@ -28,8 +28,8 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:                   # torch.cuda.current_stream().cuda_stream, without its object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -190,24 +190,32 @@ def hs_sparse_mla_noalloc_max_workspace() -> int:
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 
 
-def _operand(t, what: str, dtypes, contiguous: bool = True):
+def _operand(t, what: str, dtypes, device: int | None = None, contiguous: bool = True):
     """The address of an operand of the latent-cache calls: a CUDA tensor of one
-    of ``dtypes`` on the current device, an address (int), or None."""
+    of ``dtypes`` on the current device (``device``, for who asked already), an
+    address (int), or None."""
     if t is None or isinstance(t, int):
         return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"cannot pass {type(t)} as {what}")
     if t.dtype not in dtypes:
         raise TypeError(f"{what} is {t.dtype}, not {dtypes[0]}")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    at = t.get_device()                  # -1: not a CUDA tensor
+    if at < 0 or at != (torch.cuda.current_device() if device is None else device):
         raise ValueError(f"{what} is on {t.device}, not on the current CUDA device")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
 
 
+def _device(t) -> int | None:
+    """The current device, asked for once a call; None where ``t`` tells already
+    that the call will be refused, or is no tensor."""
+    return torch.cuda.current_device() if isinstance(t, torch.Tensor) and t.is_cuda else None
+
+
 def _shaped(t, what: str, shape: tuple) -> None:
-    if isinstance(t, torch.Tensor) and tuple(t.shape) != shape:
+    if isinstance(t, torch.Tensor) and t.shape != shape:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, not {shape}")
 
 
@@ -226,25 +234,30 @@ def append_of(num_tokens: int, token_req, positions, latent, rope, rope_freq,
     if (q_rope is None) != (q_out is None):
         raise ValueError("q_rope and q_out go together")
     T = num_tokens
-    heads = 0 if q_rope is None else q_rope.shape[1]
-    for t, what, shape in ((token_req, "token_req", (T,)), (positions, "positions", (T,)),
-                           (latent, "latent", (T, 512)), (rope, "rope", (T, 64)),
-                           (rope_freq, "rope_freq", (32,)), (q_rope, "q_rope", (T, heads, 64)),
-                           (q_out, "q_out", (T, heads, 64))):
-        _shaped(t, what, shape)
-    for t, what in ((latent, "latent"), (rope, "rope"), (q_rope, "q_rope"), (q_out, "q_out")):
-        if t is not None and t.stride(-1) != 1:
+    _shaped(token_req, "token_req", (T,))
+    _shaped(positions, "positions", (T,))
+    _shaped(latent, "latent", (T, 512))
+    _shaped(rope, "rope", (T, 64))
+    _shaped(rope_freq, "rope_freq", (32,))
+    here, i32 = _device(latent), (torch.int32,)
+    strides = [latent.stride(), rope.stride()]
+    heads = 0
+    if q_rope is not None:
+        heads = q_rope.shape[1]
+        _shaped(q_rope, "q_rope", (T, heads, 64))
+        _shaped(q_out, "q_out", (T, heads, 64))
+        strides += [q_rope.stride(), q_out.stride()]
+    for s, what in zip(strides, ("latent", "rope", "q_rope", "q_out")):
+        if s[-1] != 1:
             raise ValueError(f"{what}'s last dimension must be contiguous")
-    i32 = (torch.int32,)
-    a = HsAppend(T, heads, _operand(token_req, "token_req", i32),
-                 _operand(positions, "positions", i32),
-                 _operand(latent, "latent", _BF16, False), latent.stride(0),
-                 _operand(rope, "rope", _BF16, False), rope.stride(0),
-                 _operand(rope_freq, "rope_freq", (torch.float64,)),
-                 _operand(q_rope, "q_rope", _BF16, False),
-                 q_rope.stride(0) if heads else 0, q_rope.stride(1) if heads else 0,
-                 _operand(q_out, "q_out", _BF16, False),
-                 q_out.stride(0) if heads else 0, q_out.stride(1) if heads else 0,
+    q, o = strides[2:] if heads else ((0, 0), (0, 0))
+    a = HsAppend(T, heads, _operand(token_req, "token_req", i32, here),
+                 _operand(positions, "positions", i32, here),
+                 _operand(latent, "latent", _BF16, here, False), strides[0][0],
+                 _operand(rope, "rope", _BF16, here, False), strides[1][0],
+                 _operand(rope_freq, "rope_freq", (torch.float64,), here),
+                 _operand(q_rope, "q_rope", _BF16, here, False), q[0], q[1],
+                 _operand(q_out, "q_out", _BF16, here, False), o[0], o[1],
                  1 if rope_interleaved else 0, 0)
     a.tensors = (token_req, positions, latent, rope, rope_freq, q_rope, q_out)
     return a
