@@ -27,6 +27,9 @@ hs_status row_format(const hs_layout* lay, bool* fp4) {
 
 bool aligned4(const void* p) { return ((uintptr_t)p & 3) == 0; }
 
+// Whether n (> 1) pieces of 64 values a stride apart overlap.
+bool overlaps(int32_t n, int64_t stride) { return n > 1 && stride < 64; }
+
 bool bad_stride(int64_t stride, int64_t multiple) { return stride < 0 || stride % multiple != 0; }
 
 }  // namespace
@@ -57,7 +60,8 @@ hs_status hs_mla_append(const hs_layout* layout, const hs_batch* batch, int32_t 
   if (a.num_heads > 0 &&
       (!a.q_rope || !a.q_out || !aligned16(a.q_rope) || !aligned16(a.q_out) ||
        bad_stride(a.q_token_stride, 8) || bad_stride(a.q_head_stride, 8) ||
-       bad_stride(a.q_out_token_stride, 8) || bad_stride(a.q_out_head_stride, 8)))
+       bad_stride(a.q_out_token_stride, 8) || bad_stride(a.q_out_head_stride, 8) ||
+       overlaps(a.num_tokens, a.q_out_token_stride) || overlaps(a.num_heads, a.q_out_head_stride)))
     return HS_ERR_INVALID_ARGUMENT;
   hs::AppendParams p{};
   p.pool = batch->kv_pool + (int64_t)layer * layout->pool_layer_stride;

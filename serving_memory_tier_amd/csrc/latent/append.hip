@@ -34,6 +34,7 @@
 #include <stdint.h>
 
 #include "latent.h"
+#include "parts.h"
 
 namespace hs {
 namespace {
@@ -43,19 +44,6 @@ constexpr int kLatent = 512;
 constexpr int kPairs = 32;                     // rope pairs
 constexpr int kHeadsPerRound = kThreads / 8;   // a thread rotates 8 values of a head
 constexpr int kRounds = 4;                     // query loads in flight a thread
-
-typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
-typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
-typedef __attribute__((ext_vector_type(2))) float f32x2;
-typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
-
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) {
-  return __builtin_bit_cast(float, w & 0xffff0000u);
-}
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
-}
 
 // Quantises lane l's eight latent values (wave-wide) into the row, and writes
 // the values that the codes stand for.

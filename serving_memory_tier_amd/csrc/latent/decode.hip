@@ -38,7 +38,9 @@
 // Rounding: scores, softmax and outputs in float32; the probabilities times
 // the FP8 scales are rounded to bfloat16 for the MFMAs (half steps of 2^-8 that
 // average over the keys); key splits hand over their normalised outputs in
-// half precision (2^-11), merged in float32; out is rounded to bfloat16.
+// bfloat16 (half steps of 2^-8 that average over the splits; half precision
+// would be finer but has not the range of latent values), merged in float32; out
+// is rounded to bfloat16.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -114,35 +116,26 @@ __device__ __forceinline__ void finish(const DecodeParams& p, const Share& sh, c
   if (m < 0) return;
   l_run += __shfl_xor(l_run, 32);              // the same query row
   const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-  const int d0 = half * 256 + 4 * hi;
   const int64_t mrow = (int64_t)sh.item * p.rows + m;
-  if (p.splits == 1) {
-    uint16_t* out = p.out + mrow * kLatent + d0;
-#pragma unroll
-    for (int dt = 0; dt < 8; ++dt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<u32x2*>(out + 32 * dt + 8 * i) =
-            u32x2{bf16_pair(o[dt][4 * i] * inv, o[dt][4 * i + 1] * inv),
-                  bf16_pair(o[dt][4 * i + 2] * inv, o[dt][4 * i + 3] * inv)};
-    if (half == 0 && hi == 0)
-      p.lse[mrow] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) / kLog2e;
-    return;
-  }
   const int64_t ps = ((int64_t)sh.item * p.splits + sh.split) * p.rows + m;
   if (half == 0 && hi == 0) {
-    p.part_ml[2 * ps] = m_run;
-    p.part_ml[2 * ps + 1] = l_run;
+    if (p.splits == 1) {
+      p.lse[mrow] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) / kLog2e;
+    } else {
+      p.part_ml[2 * ps] = m_run;
+      p.part_ml[2 * ps + 1] = l_run;
+    }
   }
-  if (l_run == 0.f) return;                    // the merge does not read it
-  uint16_t* po = p.part_o + ps * kLatent + d0;
+  if (p.splits > 1 && l_run == 0.f) return;    // the merge does not read it
+  uint16_t* out = (p.splits == 1 ? p.out + mrow * kLatent : p.part_o + ps * kLatent) + half * 256 +
+                  4 * hi;
 #pragma unroll
   for (int dt = 0; dt < 8; ++dt)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<f16x4*>(po + 32 * dt + 8 * i) =
-          f16x4{(_Float16)(o[dt][4 * i] * inv), (_Float16)(o[dt][4 * i + 1] * inv),
-                (_Float16)(o[dt][4 * i + 2] * inv), (_Float16)(o[dt][4 * i + 3] * inv)};
+      *reinterpret_cast<u32x2*>(out + 32 * dt + 8 * i) =
+          u32x2{bf16_pair(o[dt][4 * i] * inv, o[dt][4 * i + 1] * inv),
+                bf16_pair(o[dt][4 * i + 2] * inv, o[dt][4 * i + 3] * inv)};
 }
 
 // ------------------------------------------------------------ 4-bit rows
@@ -232,7 +225,7 @@ struct Fetch4 {
       const int q = tid + T * i, k = q / kLat, pc = q % kLat;
       u32x4 w = (there >> i) & 1 ? lat[i] : u32x4{0u, 0u, 0u, 0u};
       uint32_t sb = (there >> i) & 1 ? (scale[i] >> (8 * (pc & 3))) & 255u : 127u;
-      if (sanitize && k >= from && sb == 255u) {
+      if (sanitize && k >= from && bad_fp4(w, sb)) {
         ids[k] = kBad;
         w = u32x4{0u, 0u, 0u, 0u};
         sb = 127u;
@@ -590,11 +583,11 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(DecodeParams p) {
   const int64_t ps0 = item * p.splits * p.rows + m;
   // eight splits' outputs at a time, the first ones beside the sums; one that saw
   // nothing was not written, and has no weight
-  f16x8 h[8];
+  u32x4 h[8];
   auto read = [&](int sp) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      h[j] = *reinterpret_cast<const f16x8*>(
+      h[j] = *reinterpret_cast<const u32x4*>(
           p.part_o + (ps0 + (int64_t)min(sp + j, p.splits - 1) * p.rows) * kLatent + 8 * l);
   };
   auto sums = [&](int sp) {
@@ -623,7 +616,10 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(DecodeParams p) {
         if (x == 0.f) continue;
         sum += x;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += x * (float)h[j][i];
+        for (int i = 0; i < 4; ++i) {
+          acc[2 * i] += x * bf16_lo(h[j][i]);
+          acc[2 * i + 1] += x * bf16_hi(h[j][i]);
+        }
       }
     }
   }
@@ -694,7 +690,7 @@ size_t plan_decode(DecodeParams& p, int64_t keys) {
   const int64_t per = (blocks + best - 1) / best;              // blocks a split
   p.splits = (int32_t)(per > 0 ? (blocks + per - 1) / per : 1);
   p.keys_per_split = per * kKeys;
-  // per (item, split, row): 512 half-precision values and two floats
+  // per (item, split, row): 512 bfloat16 values and two floats
   return p.splits > 1 ? (size_t)p.items * p.splits * p.rows * (kLatent * 2 + 2 * 4) : 0;
 }
 

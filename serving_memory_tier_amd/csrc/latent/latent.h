@@ -67,7 +67,7 @@ struct DecodeParams {
   // set by plan_decode and launch_decode
   int32_t tile_rows, row_tiles, splits;  // query rows a workgroup; their tiles
   int64_t keys_per_split;   // a multiple of 32
-  uint16_t* part_o;         // [items][splits][rows][512] IEEE half, normalised
+  uint16_t* part_o;         // [items][splits][rows][512] bfloat16, normalised
   float* part_ml;           // [items][splits][rows][2] (maximum, sum)
 };
 
@@ -98,7 +98,7 @@ struct PrefillParams {
   uint16_t* out;            // [num_q][heads][128]
   // set by plan_prefill
   int32_t tile_rows, max_tiles, splits;
-  uint16_t* part_o;         // [splits][num_q][heads][128] IEEE half, normalised
+  uint16_t* part_o;         // [splits][num_q][heads][128] bfloat16, normalised
   float* part_ml;           // [splits][num_q][heads][2] (maximum, sum)
   int32_t* off;             // [reqs + 1]
   int32_t* tile_off;        // [reqs + 1]

@@ -305,27 +305,13 @@ __global__ void __launch_bounds__(kThreads, 2) decode_narrow_kernel(DecodeParams
       // FP8: 16 (2 q) + 4 g + r, then 16 more; 4-bit: 32 q + 8 g + 2 r, even and odd
       const f32x4 a = o[rt][2 * q] * inv, b = o[rt][2 * q + 1] * inv;
       const int at = 128 * w + 32 * q + (FP4 ? 8 : 4) * g;
-      if (p.splits == 1) {
-        uint16_t* out = p.out + mrow * kLatent + at;
-        if constexpr (FP4) {
-          *reinterpret_cast<u32x4*>(out) = u32x4{bf16_pair(a[0], b[0]), bf16_pair(a[1], b[1]),
-                                                 bf16_pair(a[2], b[2]), bf16_pair(a[3], b[3])};
-        } else {
-          *reinterpret_cast<u32x2*>(out) = u32x2{bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3])};
-          *reinterpret_cast<u32x2*>(out + 16) = u32x2{bf16_pair(b[0], b[1]), bf16_pair(b[2], b[3])};
-        }
+      uint16_t* out = (p.splits == 1 ? p.out + mrow * kLatent : p.part_o + ps * kLatent) + at;
+      if constexpr (FP4) {
+        *reinterpret_cast<u32x4*>(out) = u32x4{bf16_pair(a[0], b[0]), bf16_pair(a[1], b[1]),
+                                               bf16_pair(a[2], b[2]), bf16_pair(a[3], b[3])};
       } else {
-        uint16_t* po = p.part_o + ps * kLatent + at;
-        if constexpr (FP4) {
-          *reinterpret_cast<f16x8*>(po) =
-              f16x8{(_Float16)a[0], (_Float16)b[0], (_Float16)a[1], (_Float16)b[1],
-                    (_Float16)a[2], (_Float16)b[2], (_Float16)a[3], (_Float16)b[3]};
-        } else {
-          *reinterpret_cast<f16x4*>(po) =
-              f16x4{(_Float16)a[0], (_Float16)a[1], (_Float16)a[2], (_Float16)a[3]};
-          *reinterpret_cast<f16x4*>(po + 16) =
-              f16x4{(_Float16)b[0], (_Float16)b[1], (_Float16)b[2], (_Float16)b[3]};
-        }
+        *reinterpret_cast<u32x2*>(out) = u32x2{bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3])};
+        *reinterpret_cast<u32x2*>(out + 16) = u32x2{bf16_pair(b[0], b[1]), bf16_pair(b[2], b[3])};
       }
     }
   }

@@ -14,8 +14,6 @@ typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
-typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
-typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
@@ -73,6 +71,21 @@ __device__ __forceinline__ uint32_t fp4_pair(uint32_t w, float scale = 1.f) {
 __device__ __forceinline__ bf16x8 fp4x8(uint32_t w, float scale) {
   return __builtin_bit_cast(bf16x8, u32x4{fp4_pair<0>(w, scale), fp4_pair<1>(w, scale),
                                           fp4_pair<2>(w, scale), fp4_pair<3>(w, scale)});
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) {
+  return __builtin_bit_cast(float, w & 0xffff0000u);
+}
+
+// Whether 32 E2M1 values times their E8M0 scale hold a NaN, or one past the
+// range of bfloat16: 2 and up times 2^127, 4 and up times 2^126.
+__device__ __forceinline__ bool bad_fp4(u32x4 w, uint32_t scale) {
+  if (scale < 253u) return false;
+  uint32_t big = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) big |= scale == 253u ? w[j] & (w[j] << 1) : w[j];
+  return scale == 255u || (big & 0x44444444u) != 0;
 }
 
 // The larger of a lane's value and that of the lane 32 away.

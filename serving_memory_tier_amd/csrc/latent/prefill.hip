@@ -13,7 +13,8 @@
 // Rounding: latent values are exact in bfloat16 where a row's scales are powers
 // of two (as hs_mla_append writes them), rounded once otherwise; products and
 // sums in float32; the expanded keys and values, the probabilities and the
-// output are rounded to bfloat16, as a model that stores them would.
+// output are rounded to bfloat16, as a model that stores them would, and so are
+// key splits' normalised outputs (half precision has not the values' range).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -462,31 +463,20 @@ __global__ void __launch_bounds__(64 * NW, 2) prefill_attend_kernel(PrefillParam
   l_run += __shfl_xor(l_run, 32);
   const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
   const int64_t row = qrow * p.heads + head;
-  if (p.splits == 1) {
-    uint16_t* out = p.out + row * kVal + 4 * hi;
-#pragma unroll
-    for (int dt = 0; dt < 4; ++dt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<u32x2*>(out + 32 * dt + 8 * i) =
-            u32x2{bf16_pair(o[dt][4 * i] * inv, o[dt][4 * i + 1] * inv),
-                  bf16_pair(o[dt][4 * i + 2] * inv, o[dt][4 * i + 3] * inv)};
-    return;
-  }
   const int64_t ps = (int64_t)split * p.num_q * p.heads + row;
-  if (hi == 0) {
+  if (p.splits > 1 && hi == 0) {
     p.part_ml[2 * ps] = m_run;
     p.part_ml[2 * ps + 1] = l_run;
   }
-  if (l_run == 0.f) return;                    // the merge does not read it
-  uint16_t* po = p.part_o + ps * kVal + 4 * hi;
+  if (p.splits > 1 && l_run == 0.f) return;    // the merge does not read it
+  uint16_t* out = (p.splits == 1 ? p.out + row * kVal : p.part_o + ps * kVal) + 4 * hi;
 #pragma unroll
   for (int dt = 0; dt < 4; ++dt)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<f16x4*>(po + 32 * dt + 8 * i) =
-          f16x4{(_Float16)(o[dt][4 * i] * inv), (_Float16)(o[dt][4 * i + 1] * inv),
-                (_Float16)(o[dt][4 * i + 2] * inv), (_Float16)(o[dt][4 * i + 3] * inv)};
+      *reinterpret_cast<u32x2*>(out + 32 * dt + 8 * i) =
+          u32x2{bf16_pair(o[dt][4 * i] * inv, o[dt][4 * i + 1] * inv),
+                bf16_pair(o[dt][4 * i + 2] * inv, o[dt][4 * i + 3] * inv)};
 }
 
 // Merges the key splits of a (query, head), 16 lanes 8 dimensions each: with
@@ -510,9 +500,12 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(PrefillParams p) {
     if (l == 0.f) continue;                    // nothing seen there: not written
     const float x = exp2f(p.part_ml[2 * ps] - M) * l;          // NaN stays NaN
     sum += x;
-    const f16x8 h = *reinterpret_cast<const f16x8*>(p.part_o + ps * kVal + 8 * c);
+    const u32x4 h = *reinterpret_cast<const u32x4*>(p.part_o + ps * kVal + 8 * c);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] += x * (float)h[i];
+    for (int i = 0; i < 4; ++i) {
+      acc[2 * i] += x * bf16_lo(h[i]);
+      acc[2 * i + 1] += x * bf16_hi(h[i]);
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   *reinterpret_cast<u32x4*>(p.out + row * kVal + 8 * c) =

@@ -81,6 +81,8 @@ def append(**kw):
     ({}, {}, 0, dict(q_rope=0x1002), FAKE, FAKE, 1), ({}, {}, 0, dict(q_out=0x1002), FAKE, FAKE, 1),
     ({}, {}, 0, dict(q_head_stride=68), FAKE, FAKE, 1),
     ({}, {}, 0, dict(q_out_token_stride=130), FAKE, FAKE, 1),
+    ({}, {}, 0, dict(q_out_token_stride=56), FAKE, FAKE, 1),
+    ({}, {}, 0, dict(q_out_head_stride=0), FAKE, FAKE, 1),
     ({}, {}, 0, dict(rope_interleaved=2), FAKE, FAKE, 1), ({}, {}, 0, dict(reserved=1), FAKE, FAKE, 1),
     ({}, {}, 0, {}, FAKE, 0x1008, 1),
 ])
