@@ -475,7 +475,7 @@ hs_status hs_mla_append(const hs_layout* layout, const hs_batch* batch, int32_t 
  * Precision: keys and values are used exactly (an E2M1 value times a power of
  * two is a bfloat16 value), scores and sums in float32, the probabilities
  * rounded to bfloat16 for the value products, key splits merged in float32
- * from bfloat16 outputs, out rounded to bfloat16.  A selected row with a
+ * from scaled half-precision outputs, out rounded to bfloat16.  A selected row with a
  * NaN scale makes its token's outputs NaN.
  * workspace: device memory of at least hs_sparse_mla_fp4_workspace_bytes(...)
  * bytes, 16-byte aligned (may be NULL when that is 0), overwritten; calls
@@ -556,8 +556,8 @@ size_t hs_paged_mla_workspace_bytes(int32_t num_reqs, int32_t num_pos, int32_t n
  * sharing one must not overlap.
  * Precision: products and sums in float32; the latent values (where a row's
  * scale is no power of two), the expanded keys and values, the probabilities
- * and out are rounded to bfloat16, as are key splits' outputs before their
- * merge in float32.  The expanded values have to be within the range of float32.
+ * and out are rounded to bfloat16, key splits' outputs to scaled half precision
+ * before their merge in float32.  The expanded values have to be within the range of float32.
  * Errors: HS_ERR_INVALID_ARGUMENT (null or misaligned pointers with work to
  * do, a short workspace, negative sizes, num_heads < 1, a bad layer or
  * layout), HS_ERR_UNSUPPORTED (another row_bytes, over 1,048,576 heads or

@@ -37,10 +37,10 @@
 //
 // Rounding: scores, softmax and outputs in float32; the probabilities times
 // the FP8 scales are rounded to bfloat16 for the MFMAs (half steps of 2^-8 that
-// average over the keys); key splits hand over their normalised outputs in
-// bfloat16 (half steps of 2^-8 that average over the splits; half precision
-// would be finer but has not the range of latent values), merged in float32; out
-// is rounded to bfloat16.
+// average over the keys); key splits hand over their normalised outputs in half
+// precision, brought into its range by a power of two for each wave's dimensions
+// of a row (half steps of 2^-11, against bfloat16's 2^-8 at the same bytes),
+// merged in float32; out is rounded to bfloat16.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -116,26 +116,40 @@ __device__ __forceinline__ void finish(const DecodeParams& p, const Share& sh, c
   if (m < 0) return;
   l_run += __shfl_xor(l_run, 32);              // the same query row
   const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+  const int d0 = half * 256 + 4 * hi;
   const int64_t mrow = (int64_t)sh.item * p.rows + m;
-  const int64_t ps = ((int64_t)sh.item * p.splits + sh.split) * p.rows + m;
-  if (half == 0 && hi == 0) {
-    if (p.splits == 1) {
+  if (p.splits == 1) {
+    uint16_t* out = p.out + mrow * kLatent + d0;
+#pragma unroll
+    for (int dt = 0; dt < 8; ++dt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<u32x2*>(out + 32 * dt + 8 * i) =
+            u32x2{bf16_pair(o[dt][4 * i] * inv, o[dt][4 * i + 1] * inv),
+                  bf16_pair(o[dt][4 * i + 2] * inv, o[dt][4 * i + 3] * inv)};
+    if (half == 0 && hi == 0)
       p.lse[mrow] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) / kLog2e;
-    } else {
-      p.part_ml[2 * ps] = m_run;
-      p.part_ml[2 * ps + 1] = l_run;
-    }
+    return;
   }
-  if (p.splits > 1 && l_run == 0.f) return;    // the merge does not read it
-  uint16_t* out = (p.splits == 1 ? p.out + mrow * kLatent : p.part_o + ps * kLatent) + half * 256 +
-                  4 * hi;
+  const int64_t ps = ((int64_t)sh.item * p.splits + sh.split) * p.rows + m;
+  float* ml = p.part_ml + kPartFloats * ps;
+  if (half == 0 && hi == 0) *reinterpret_cast<f32x2*>(ml) = f32x2{m_run, l_run};
+  if (l_run == 0.f) return;                    // the merge does not read it
+  float most = 0.f;
+#pragma unroll
+  for (int dt = 0; dt < 8; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(o[dt][i]));
+  const int e = half_exponent(max_halves(most) * inv);
+  if (hi == 0) *reinterpret_cast<f32x2*>(ml + 2 + 2 * half) = f32x2{ldexpf(1.f, e), ldexpf(1.f, e)};
+  const float f = ldexpf(inv, -e);
+  uint16_t* po = p.part_o + ps * kLatent + d0;
 #pragma unroll
   for (int dt = 0; dt < 8; ++dt)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<u32x2*>(out + 32 * dt + 8 * i) =
-          u32x2{bf16_pair(o[dt][4 * i] * inv, o[dt][4 * i + 1] * inv),
-                bf16_pair(o[dt][4 * i + 2] * inv, o[dt][4 * i + 3] * inv)};
+      *reinterpret_cast<f16x4*>(po + 32 * dt + 8 * i) = half4(
+          o[dt][4 * i] * f, o[dt][4 * i + 1] * f, o[dt][4 * i + 2] * f, o[dt][4 * i + 3] * f);
 }
 
 // ------------------------------------------------------------ 4-bit rows
@@ -583,16 +597,19 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(DecodeParams p) {
   const int64_t ps0 = item * p.splits * p.rows + m;
   // eight splits' outputs at a time, the first ones beside the sums; one that saw
   // nothing was not written, and has no weight
-  u32x4 h[8];
+  f16x8 h[8];
+  float scale[8];
   auto read = [&](int sp) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      h[j] = *reinterpret_cast<const u32x4*>(
-          p.part_o + (ps0 + (int64_t)min(sp + j, p.splits - 1) * p.rows) * kLatent + 8 * l);
+    for (int j = 0; j < 8; ++j) {
+      const int64_t ps = ps0 + (int64_t)min(sp + j, p.splits - 1) * p.rows;
+      h[j] = *reinterpret_cast<const f16x8*>(p.part_o + ps * kLatent + 8 * l);
+      scale[j] = p.part_ml[kPartFloats * ps + 2 + (l >> 4)];
+    }
   };
   auto sums = [&](int sp) {
     return sp < p.splits
-               ? *reinterpret_cast<const f32x2*>(p.part_ml + 2 * (ps0 + (int64_t)sp * p.rows))
+               ? *reinterpret_cast<const f32x2*>(p.part_ml + kPartFloats * (ps0 + (int64_t)sp * p.rows))
                : f32x2{-INFINITY, 0.f};
   };
   f32x2 ml = sums(l);
@@ -615,11 +632,9 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(DecodeParams p) {
         const float x = __shfl(wgt, j0 + j);   // 0 past the last split
         if (x == 0.f) continue;
         sum += x;
+        const float y = x * scale[j];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[2 * i] += x * bf16_lo(h[j][i]);
-          acc[2 * i + 1] += x * bf16_hi(h[j][i]);
-        }
+        for (int i = 0; i < 8; ++i) acc[i] += y * (float)h[j][i];
       }
     }
   }
@@ -690,8 +705,7 @@ size_t plan_decode(DecodeParams& p, int64_t keys) {
   const int64_t per = (blocks + best - 1) / best;              // blocks a split
   p.splits = (int32_t)(per > 0 ? (blocks + per - 1) / per : 1);
   p.keys_per_split = per * kKeys;
-  // per (item, split, row): 512 bfloat16 values and two floats
-  return p.splits > 1 ? (size_t)p.items * p.splits * p.rows * (kLatent * 2 + 2 * 4) : 0;
+  return p.splits > 1 ? (size_t)p.items * p.splits * p.rows * (kLatent * 2 + kPartFloats * 4) : 0;
 }
 
 bool decode_fits(const DecodeParams& p) {

@@ -13,6 +13,10 @@ constexpr int kLatent = 512;
 constexpr int kDim = 576;
 constexpr int32_t kBad = -2;                 // in place of a fetched row's id: see sanitize_rows
 
+// A (split, query row)'s floats in part_ml: its maximum, its sum, and the scales of
+// its four times 128 partial outputs.
+constexpr int kPartFloats = 6;
+
 // The lists of a workgroup of ROWS query rows.
 template <int ROWS>
 struct Lists {

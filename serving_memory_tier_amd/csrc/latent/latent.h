@@ -67,8 +67,8 @@ struct DecodeParams {
   // set by plan_decode and launch_decode
   int32_t tile_rows, row_tiles, splits;  // query rows a workgroup; their tiles
   int64_t keys_per_split;   // a multiple of 32
-  uint16_t* part_o;         // [items][splits][rows][512] bfloat16, normalised
-  float* part_ml;           // [items][splits][rows][2] (maximum, sum)
+  uint16_t* part_o;         // [items][splits][rows][512] IEEE half, normalised and scaled
+  float* part_ml;           // [items][splits][rows][6]: maximum, sum, four scales
 };
 
 // Sets the launch shape for items of about `keys` keys; returns the workspace's bytes.
@@ -98,8 +98,8 @@ struct PrefillParams {
   uint16_t* out;            // [num_q][heads][128]
   // set by plan_prefill
   int32_t tile_rows, max_tiles, splits;
-  uint16_t* part_o;         // [splits][num_q][heads][128] bfloat16, normalised
-  float* part_ml;           // [splits][num_q][heads][2] (maximum, sum)
+  uint16_t* part_o;         // [splits][num_q][heads][128] IEEE half, normalised and scaled
+  float* part_ml;           // [splits][num_q][heads][3]: maximum, sum, scale
   int32_t* off;             // [reqs + 1]
   int32_t* tile_off;        // [reqs + 1]
   uint8_t* flags;           // [num_kv]

@@ -286,8 +286,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_narrow_kernel(DecodeParams
             l_run[i] == 0.f ? -INFINITY : (m_run[i] + log2f(l_run[i])) / kLog2e;
       } else {
         const int64_t ps = ((int64_t)sh.item * p.splits + sh.split) * p.rows + m;
-        p.part_ml[2 * ps] = m_run[i];
-        p.part_ml[2 * ps + 1] = l_run[i];
+        *reinterpret_cast<f32x2*>(p.part_ml + kPartFloats * ps) = f32x2{m_run[i], l_run[i]};
       }
     }
   }
@@ -300,18 +299,42 @@ __global__ void __launch_bounds__(kThreads, 2) decode_narrow_kernel(DecodeParams
     const int64_t mrow = (int64_t)sh.item * p.rows + m;
     const int64_t ps = ((int64_t)sh.item * p.splits + sh.split) * p.rows + m;
     if (p.splits > 1 && sum == 0.f) continue;  // the merge does not read it
+    float f = inv;
+    if (p.splits > 1) {
+      float most = 0.f;                        // of the row's 128 dimensions: four lanes'
+#pragma unroll
+      for (int dt = 0; dt < 8; ++dt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) most = fmaxf(most, fabsf(o[rt][dt][r]));
+      most = fmaxf(most, __shfl_xor(most, 16));
+      most = fmaxf(most, __shfl_xor(most, 32));
+      const int e = half_exponent(most * inv);
+      if (g == 0) p.part_ml[kPartFloats * ps + 2 + w] = ldexpf(1.f, e);
+      f = ldexpf(inv, -e);
+    }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       // FP8: 16 (2 q) + 4 g + r, then 16 more; 4-bit: 32 q + 8 g + 2 r, even and odd
-      const f32x4 a = o[rt][2 * q] * inv, b = o[rt][2 * q + 1] * inv;
+      const f32x4 a = o[rt][2 * q] * f, b = o[rt][2 * q + 1] * f;
       const int at = 128 * w + 32 * q + (FP4 ? 8 : 4) * g;
-      uint16_t* out = (p.splits == 1 ? p.out + mrow * kLatent : p.part_o + ps * kLatent) + at;
-      if constexpr (FP4) {
-        *reinterpret_cast<u32x4*>(out) = u32x4{bf16_pair(a[0], b[0]), bf16_pair(a[1], b[1]),
-                                               bf16_pair(a[2], b[2]), bf16_pair(a[3], b[3])};
+      if (p.splits == 1) {
+        uint16_t* out = p.out + mrow * kLatent + at;
+        if constexpr (FP4) {
+          *reinterpret_cast<u32x4*>(out) = u32x4{bf16_pair(a[0], b[0]), bf16_pair(a[1], b[1]),
+                                                 bf16_pair(a[2], b[2]), bf16_pair(a[3], b[3])};
+        } else {
+          *reinterpret_cast<u32x2*>(out) = u32x2{bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3])};
+          *reinterpret_cast<u32x2*>(out + 16) = u32x2{bf16_pair(b[0], b[1]), bf16_pair(b[2], b[3])};
+        }
       } else {
-        *reinterpret_cast<u32x2*>(out) = u32x2{bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3])};
-        *reinterpret_cast<u32x2*>(out + 16) = u32x2{bf16_pair(b[0], b[1]), bf16_pair(b[2], b[3])};
+        uint16_t* po = p.part_o + ps * kLatent + at;
+        if constexpr (FP4) {
+          *reinterpret_cast<f16x4*>(po) = half4(a[0], b[0], a[1], b[1]);
+          *reinterpret_cast<f16x4*>(po + 4) = half4(a[2], b[2], a[3], b[3]);
+        } else {
+          *reinterpret_cast<f16x4*>(po) = half4(a[0], a[1], a[2], a[3]);
+          *reinterpret_cast<f16x4*>(po + 16) = half4(b[0], b[1], b[2], b[3]);
+        }
       }
     }
   }

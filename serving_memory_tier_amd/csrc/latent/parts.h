@@ -21,6 +21,8 @@ typedef __attribute__((ext_vector_type(2))) int i32x2;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
 typedef __attribute__((ext_vector_type(2))) float f32x2;
+typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 
 // Within each 16 lanes, lane c receives element c % 4 of the 8-byte vectors at
 // the addresses of lanes 4 j + c / 4, j = 0..3.
@@ -93,6 +95,17 @@ __device__ __forceinline__ float max_halves(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x),
                                                   __builtin_bit_cast(uint32_t, x), false, false);
   return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+
+// The power of two (its exponent) that brings values of magnitude `most` at the
+// largest to [1, 2), where half precision keeps 11 bits of them.
+__device__ __forceinline__ int half_exponent(float most) {
+  // (no further than what the factor 2^-e allows)
+  return most > 0.f && most < INFINITY ? max(__builtin_amdgcn_frexp_expf(most) - 1, -120) : 0;
+}
+
+__device__ __forceinline__ f16x4 half4(float a, float b, float c, float d) {
+  return f16x4{(_Float16)a, (_Float16)b, (_Float16)c, (_Float16)d};
 }
 
 // The thread's number, opaque to the compiler: what it addresses with it is

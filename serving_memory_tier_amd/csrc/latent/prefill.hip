@@ -13,8 +13,9 @@
 // Rounding: latent values are exact in bfloat16 where a row's scales are powers
 // of two (as hs_mla_append writes them), rounded once otherwise; products and
 // sums in float32; the expanded keys and values, the probabilities and the
-// output are rounded to bfloat16, as a model that stores them would, and so are
-// key splits' normalised outputs (half precision has not the values' range).
+// output are rounded to bfloat16, as a model that stores them would; key splits'
+// normalised outputs to half precision, brought into its range by a power of two
+// a row.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -30,6 +31,7 @@ namespace {
 constexpr int kNope = 128, kRopeDim = 64, kVal = 128;
 constexpr int kQ = kNope + kRopeDim;         // 192
 constexpr int kHeadRow = kNope + kVal;       // 256 values a (head, token)
+constexpr int kPartFloats = 3;               // a split's, a row: maximum, sum, the values' scale
 
 // ------------------------------------------------------------- offsets
 
@@ -463,20 +465,38 @@ __global__ void __launch_bounds__(64 * NW, 2) prefill_attend_kernel(PrefillParam
   l_run += __shfl_xor(l_run, 32);
   const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
   const int64_t row = qrow * p.heads + head;
-  const int64_t ps = (int64_t)split * p.num_q * p.heads + row;
-  if (p.splits > 1 && hi == 0) {
-    p.part_ml[2 * ps] = m_run;
-    p.part_ml[2 * ps + 1] = l_run;
+  if (p.splits == 1) {
+    uint16_t* out = p.out + row * kVal + 4 * hi;
+#pragma unroll
+    for (int dt = 0; dt < 4; ++dt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<u32x2*>(out + 32 * dt + 8 * i) =
+            u32x2{bf16_pair(o[dt][4 * i] * inv, o[dt][4 * i + 1] * inv),
+                  bf16_pair(o[dt][4 * i + 2] * inv, o[dt][4 * i + 3] * inv)};
+    return;
   }
-  if (p.splits > 1 && l_run == 0.f) return;    // the merge does not read it
-  uint16_t* out = (p.splits == 1 ? p.out + row * kVal : p.part_o + ps * kVal) + 4 * hi;
+  const int64_t ps = (int64_t)split * p.num_q * p.heads + row;
+  float most = 0.f;
+#pragma unroll
+  for (int dt = 0; dt < 4; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(o[dt][i]));
+  const int e = half_exponent(max_halves(most) * inv);
+  if (hi == 0) {
+    p.part_ml[kPartFloats * ps] = m_run;
+    p.part_ml[kPartFloats * ps + 1] = l_run;
+    p.part_ml[kPartFloats * ps + 2] = ldexpf(1.f, e);
+  }
+  if (l_run == 0.f) return;                    // the merge does not read it
+  const float f = ldexpf(inv, -e);
+  uint16_t* po = p.part_o + ps * kVal + 4 * hi;
 #pragma unroll
   for (int dt = 0; dt < 4; ++dt)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<u32x2*>(out + 32 * dt + 8 * i) =
-          u32x2{bf16_pair(o[dt][4 * i] * inv, o[dt][4 * i + 1] * inv),
-                bf16_pair(o[dt][4 * i + 2] * inv, o[dt][4 * i + 3] * inv)};
+      *reinterpret_cast<f16x4*>(po + 32 * dt + 8 * i) = half4(
+          o[dt][4 * i] * f, o[dt][4 * i + 1] * f, o[dt][4 * i + 2] * f, o[dt][4 * i + 3] * f);
 }
 
 // Merges the key splits of a (query, head), 16 lanes 8 dimensions each: with
@@ -491,21 +511,19 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(PrefillParams p) {
   float M = -INFINITY;
   for (int sp = 0; sp < p.splits; ++sp) {
     const int64_t ps = (int64_t)sp * rows + row;
-    if (p.part_ml[2 * ps + 1] != 0.f) M = fmaxf(M, p.part_ml[2 * ps]);
+    if (p.part_ml[kPartFloats * ps + 1] != 0.f) M = fmaxf(M, p.part_ml[kPartFloats * ps]);
   }
   float sum = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int sp = 0; sp < p.splits; ++sp) {
     const int64_t ps = (int64_t)sp * rows + row;
-    const float l = p.part_ml[2 * ps + 1];
-    if (l == 0.f) continue;                    // nothing seen there: not written
-    const float x = exp2f(p.part_ml[2 * ps] - M) * l;          // NaN stays NaN
+    const float* ml = p.part_ml + kPartFloats * ps;
+    if (ml[1] == 0.f) continue;                // nothing seen there: not written
+    const float x = exp2f(ml[0] - M) * ml[1];  // NaN stays NaN
     sum += x;
-    const u32x4 h = *reinterpret_cast<const u32x4*>(p.part_o + ps * kVal + 8 * c);
+    const float y = x * ml[2];
+    const f16x8 h = *reinterpret_cast<const f16x8*>(p.part_o + ps * kVal + 8 * c);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      acc[2 * i] += x * bf16_lo(h[i]);
-      acc[2 * i + 1] += x * bf16_hi(h[i]);
-    }
+    for (int i = 0; i < 8; ++i) acc[i] += y * (float)h[i];
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   *reinterpret_cast<u32x4*>(p.out + row * kVal + 8 * c) =
@@ -566,7 +584,7 @@ size_t plan_prefill(PrefillParams& p, void* workspace) {
   p.heads_kv = reinterpret_cast<uint16_t*>(take(H * kv * kHeadRow * 2));
   if (p.splits > 1) {
     p.part_o = reinterpret_cast<uint16_t*>(take((size_t)p.splits * nq * H * kVal * 2));
-    p.part_ml = reinterpret_cast<float*>(take((size_t)p.splits * nq * H * 2 * 4));
+    p.part_ml = reinterpret_cast<float*>(take((size_t)p.splits * nq * H * kPartFloats * 4));
   }
   return n;
 }

@@ -3,11 +3,13 @@ oracle, within bounds the arithmetic fixes.  With A = sum_j p_j |v_j| (each
 value dimension) and S the largest scale * <|q|, |k_j|>:
   - scores accumulate 576 float32 products: off by at most 600 * 2^-24 * S = e;
   - the probabilities times scales are rounded to bfloat16: 2^-8 A;
-  - a split's normalised output is rounded to bfloat16: 2^-8 A;
+  - a split's normalised output is rounded to half precision, scaled so that its
+    largest value is in [1, 2): 2^-11 A, or half a step of its least, 2^-25 of
+    that scale, which is at most the row's largest A;
   - the output is rounded to bfloat16: 2^-8 |out|;
-so |d out| <= (2^-8 + 2^-8 + 2 e) A + 2^-8 |out| + 2^-30 (probabilities below
-float32's range), and |d lse| <= e + 2^-20 |lse| + 2^-20 (the sum, its logarithm
-and the two products with log2 e)."""
+so |d out| <= (2^-8 + 2^-11 + 2 e) A + 2^-25 max A + 2^-8 |out| + 2^-30
+(probabilities below float32's range), and |d lse| <= e + 2^-20 |lse| + 2^-20
+(the sum, its logarithm and the two products with log2 e)."""
 
 from __future__ import annotations
 
@@ -66,7 +68,8 @@ def bound(q, ids, pool, seen, scale, out, lse):
     a, _ = ol.attend(q, k, np.abs(v), seen, scale)
     s = (np.where(seen, scale * (np.abs(q) @ np.abs(k).T), 0)).max(1, initial=0)
     e = 600 * 2.0 ** -24 * s[:, None]
-    return ((2.0 ** -7 + 2 * e) * a + 2.0 ** -8 * np.abs(out) + 2.0 ** -30,
+    return ((2.0 ** -8 + 2.0 ** -11 + 2 * e) * a + 2.0 ** -25 * a.max(1, keepdims=True)
+            + 2.0 ** -8 * np.abs(out) + 2.0 ** -30,
             e[:, 0] + 2.0 ** -20 * np.abs(np.where(np.isfinite(lse), lse, 0)) + 2.0 ** -20)
 
 
@@ -301,7 +304,7 @@ def test_split_outputs_keep_their_range(fmt, H, power):
     import serving_memory_tier_amd as hs
     rs = np.random.default_rng(6)
     ctx, page = 1500, 64
-    assert hs.hs_paged_mla_workspace_bytes(1, 1, H, ctx) > H * 1032      # more than one
+    assert hs.hs_paged_mla_workspace_bytes(1, 1, H, ctx) > H * 1048      # more than one
     pool = make_pool(rs, 24 * page, fmt)
     if fmt == 400:
         pool[:, 256:272] += np.uint8(power % 256)

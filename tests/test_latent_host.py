@@ -222,9 +222,9 @@ def test_workspace_sizes(lib):
     assert hs.hs_paged_mla_workspace_bytes(4, 1, 16, -1) == 0
     assert hs.hs_mla_prefill_workspace_bytes(1, 0, 100, 4) == 0
     assert hs.hs_mla_prefill_workspace_bytes(1, 10, -1, 4) == 0
-    # a split's row: 512 halves and two floats
+    # a split's row: 512 halves and six floats
     for n, heads, k in ((1, 16, 4096), (32, 128, 2048), (3, 129, 70000)):
-        assert hs.hs_sparse_mla_fp4_workspace_bytes(n, heads, k) % (n * heads * 1032) == 0
+        assert hs.hs_sparse_mla_fp4_workspace_bytes(n, heads, k) % (n * heads * 1048) == 0
     # the expanded keys and values at least, whatever the requests
     assert hs.hs_mla_prefill_workspace_bytes(3, 100, 1000, 8) >= 1000 * 8 * 512
     # sizes beyond 32 bits
