@@ -6,8 +6,11 @@ memory and streams.  The names mirror the C ABI in ``include/hisparse.h``:
 ``hs_resolve``, ``hs_gather``, ``hs_offload_prefix_pages``, ``hs_plan_replay``,
 ``hs_resolve_grouped`` (layers sharing a top-K list),
 the resolver's stages (``hs_resolve_decide``, ``hs_resolve_fetch``,
-``hs_resolve_move``, ``hs_resolve_commit``), plus pinned host-pool helpers.  There is no fallback: if the library is
-missing or fails to load, every call raises.
+``hs_resolve_move``, ``hs_resolve_commit``), the consumers and the writer of the
+latent rows (``hs_sparse_mla_decode``, ``hs_mla_append``,
+``hs_sparse_mla_decode_fp4``, ``hs_paged_mla_decode``, ``hs_mla_prefill``), plus
+pinned host-pool helpers.  There is no fallback: if the library is missing or
+fails to load, every call raises.
 """
 
 from ._lib import (EXPORTS, HS_ERR_HIP, HS_ERR_INVALID_ARGUMENT, HS_ERR_LAUNCH,

@@ -28,12 +28,25 @@
 //     key, and the transposed operand pairs keys, so scaling there would take
 //     a multiplication and a packing of every probability for each 32
 //     dimensions.  Two blocks are resident, the one after is in registers; two
-//     barriers a block.
+//     barriers a block.  The two waves of a SIMD run half a block apart, so that
+//     one's scores meet the other's softmax and value products.
 //   FP8 rows go from the pool into LDS as they are, with no register between
-//     (three blocks resident, one barrier a block), and are converted at each
-//     use, exactly; their float32 scales, one per 128 values, multiply the
-//     partial scores and the probabilities.  Converted copies beside the
-//     scales' accumulators would not fit the registers.
+//     (three blocks resident, two barriers a block), and are converted at each
+//     use, exactly; their float32 scales, one per 128 values, copied beside the
+//     rows once a block, multiply the partial scores and the probabilities.
+//     Converted copies beside the scales' accumulators would not fit the
+//     registers.
+//
+// Bound: a block's LDS reads (18 KB of keys and 16 KB of values a wave, the
+// transposing reads at half the rate of the others), its MFMAs and the steps
+// between them, which two waves a SIMD overlap in part (no LDS bank conflict is
+// left over 4-bit rows).  512 tokens x 128 heads x 2,048 4-bit rows: 353 us, 811
+// TFLOP/s, 37 % of what a loop of these MFMAs alone reaches (2,170); a large matrix
+// product of the library reaches 1,210 to 1,330.  32 x 128 x 2,048 takes 45 us, of it the
+// merge 8 (eight splits, 34 MB written and read); 8 requests x 4 positions x 128
+// heads on up to 74,160 4-bit tokens 799 us (633 TFLOP/s; its splits fill 3.6
+// rounds of the chip and take 4); 32 x 128 heads on up to 8,192 FP8 tokens
+// 114 us (484 TFLOP/s: the conversions at use).
 //
 // Rounding: scores, softmax and outputs in float32; the probabilities times
 // the FP8 scales are rounded to bfloat16 for the MFMAs (half steps of 2^-8 that
@@ -674,11 +687,19 @@ int64_t decode_grid(const DecodeParams& p) {
 }
 
 size_t plan_decode(DecodeParams& p, int64_t keys) {
+  // The least tile that holds the rows: up to 32 the narrow kernel, up to 64 this
+  // file's with two wave pairs.  Measured with tiles of 16, 32, 64 and 128 rows, 32
+  // requests on up to 8,192 FP8 tokens: 16 heads 47, 59, 99 and 107 us; 32 heads
+  // 79, 63, 101 and 111; 64 heads 146, 109, 106 and 117; 128 heads 277, 202, 193
+  // and 125
   p.tile_rows = p.rows <= 16 ? 16 : p.rows <= 32 ? 32 : p.rows <= 64 ? 64 : 128;
   p.row_tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
   // Key splits: the fewest block times over the rounds of the chip that the
   // workgroups take (256 units, two narrow workgroups each), with some block
-  // times a workgroup for its start and end, and a merge's launch and traffic
+  // times a workgroup for its start and end, and a merge's launch and traffic.
+  // 5 tokens x 16 heads x 1,000 rows with 8, 16 and 32 splits: 13.8, 11.8, 12.7 us;
+  // 32 x 128 x 2,048 with 2, 4 and 8: 95, 63, 50; one request of 16 heads on 8,192
+  // tokens with 16, 32 and 64: 35, 24, 21
   const int64_t base = (int64_t)p.items * p.row_tiles;
   const int64_t blocks = (keys + kKeys - 1) / kKeys;
   const int64_t slots = p.tile_rows >= 64 ? 256 : 512;
