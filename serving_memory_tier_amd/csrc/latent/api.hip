@@ -100,7 +100,7 @@ hs_status attend(hs::DecodeParams p, bool fp4, bool paged, int64_t keys, const v
                  hipStream_t stream) {
   if (!p.q || !out || !lse || !aligned16(p.q) || !aligned16(out) || !aligned4(lse))
     return HS_ERR_INVALID_ARGUMENT;
-  const size_t need = hs::plan_decode(p, keys);
+  const size_t need = hs::plan_decode(p, keys, paged);
   if (!hs::decode_fits(p)) return HS_ERR_UNSUPPORTED;
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
     return HS_ERR_INVALID_ARGUMENT;
@@ -142,7 +142,7 @@ size_t hs_sparse_mla_fp4_workspace_bytes(int32_t num_tokens, int32_t num_heads, 
   hs::DecodeParams p{};
   p.items = num_tokens;
   p.rows = num_heads;
-  return hs::plan_decode(p, top_k);
+  return hs::plan_decode(p, top_k, false);
 }
 
 hs_status hs_paged_mla_decode(const hs_layout* layout, const hs_batch* batch, int32_t layer,
@@ -177,7 +177,7 @@ hs_status hs_paged_mla_decode(const hs_layout* layout, const hs_batch* batch, in
   p.scale = sm_scale;
   p.out = out;
   p.lse = lse;
-  // the split goes by the caller's bound, whatever the table's size: the
+  // the launch goes by the caller's bound, whatever the table's size: the
   // workspace is a matter of the call's sizes alone
   return attend(p, fp4, true, max_ctx, out, lse, workspace, workspace_bytes, "paged MLA launch",
                 stream);
@@ -191,7 +191,7 @@ size_t hs_paged_mla_workspace_bytes(int32_t num_reqs, int32_t num_pos, int32_t n
   hs::DecodeParams p{};
   p.items = num_reqs;
   p.rows = num_pos * num_heads;
-  return hs::plan_decode(p, max_ctx);
+  return hs::plan_decode(p, max_ctx, true);
 }
 
 hs_status hs_mla_prefill(const hs_layout* layout, const hs_batch* batch, int32_t layer,

@@ -144,7 +144,7 @@ __device__ __forceinline__ void finish(const DecodeParams& p, const Share& sh, c
       p.lse[mrow] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) / kLog2e;
     return;
   }
-  const int64_t ps = ((int64_t)sh.item * p.splits + sh.split) * p.rows + m;
+  const int64_t ps = sh.part * p.rows + m;
   float* ml = p.part_ml + kPartFloats * ps;
   if (half == 0 && hi == 0) *reinterpret_cast<f32x2*>(ml) = f32x2{m_run, l_run};
   if (l_run == 0.f) return;                    // the merge does not read it
@@ -607,7 +607,9 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(DecodeParams p) {
   const int64_t mrow = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (mrow >= (int64_t)p.items * p.rows) return;
   const int64_t item = mrow / p.rows, m = mrow - item * p.rows;
-  const int64_t ps0 = item * p.splits * p.rows + m;
+  const int64_t part0 = p.part_off ? p.part_off[item] : item * p.splits;
+  const int32_t splits = p.part_off ? p.part_off[item + 1] - (int32_t)part0 : p.splits;
+  const int64_t ps0 = part0 * p.rows + m;
   // eight splits' outputs at a time, the first ones beside the sums; one that saw
   // nothing was not written, and has no weight
   f16x8 h[8];
@@ -615,30 +617,30 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(DecodeParams p) {
   auto read = [&](int sp) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int64_t ps = ps0 + (int64_t)min(sp + j, p.splits - 1) * p.rows;
+      const int64_t ps = ps0 + (int64_t)min(sp + j, splits - 1) * p.rows;
       h[j] = *reinterpret_cast<const f16x8*>(p.part_o + ps * kLatent + 8 * l);
       scale[j] = p.part_ml[kPartFloats * ps + 2 + (l >> 4)];
     }
   };
   auto sums = [&](int sp) {
-    return sp < p.splits
+    return sp < splits
                ? *reinterpret_cast<const f32x2*>(p.part_ml + kPartFloats * (ps0 + (int64_t)sp * p.rows))
                : f32x2{-INFINITY, 0.f};
   };
   f32x2 ml = sums(l);
   read(0);
   float M = ml[1] != 0.f ? ml[0] : -INFINITY;
-  for (int sp = l + 64; sp < p.splits; sp += 64) {
+  for (int sp = l + 64; sp < splits; sp += 64) {
     const f32x2 v = sums(sp);
     if (v[1] != 0.f) M = fmaxf(M, v[0]);
   }
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) M = fmaxf(M, __shfl_xor(M, d));
   float sum = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int s0 = 0; s0 < p.splits; s0 += 64) {
+  for (int s0 = 0; s0 < splits; s0 += 64) {
     if (s0 > 0) ml = sums(s0 + l);
     const float wgt = ml[1] != 0.f ? exp2f(ml[0] - M) * ml[1] : 0.f;    // NaN stays NaN
-    for (int j0 = 0; j0 < min(64, p.splits - s0); j0 += 8) {
+    for (int j0 = 0; j0 < min(64, splits - s0); j0 += 8) {
       if (s0 + j0 > 0) read(s0 + j0);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -686,7 +688,13 @@ int64_t decode_grid(const DecodeParams& p) {
   return ((int64_t)p.items * p.splits + 7) / 8 * 8 * p.row_tiles;
 }
 
-size_t plan_decode(DecodeParams& p, int64_t keys) {
+// Whether the kernel deals out the splits by the contexts: a wave's lanes a request
+// each, and splits of more than the least, one block.
+static bool dealt_out(const DecodeParams& p, bool paged) {
+  return paged && p.items <= 64 && p.splits > 1 && p.keys_per_split > kKeys;
+}
+
+size_t plan_decode(DecodeParams& p, int64_t keys, bool paged) {
   // The least tile that holds the rows: up to 32 the narrow kernel, up to 64 this
   // file's with two wave pairs.  Measured with tiles of 16, 32, 64 and 128 rows, 32
   // requests on up to 8,192 FP8 tokens: 16 heads 47, 59, 99 and 107 us; 32 heads
@@ -706,9 +714,11 @@ size_t plan_decode(DecodeParams& p, int64_t keys) {
   const int64_t least = (blocks * kKeys + kDecodeSplitKeys - 1) / kDecodeSplitKeys;
   int64_t best = 1;
   double best_t = 1e300;
-  // as few as may be; as many as fill 1 to 4 rounds; a half and a quarter of the blocks
+  const int64_t full = base * least / slots;   // rounds that the fewest splits fill
+  // as few as may be; as many as fill up to four rounds more; a half and a quarter
+  // of the blocks
   for (int r = 0; r <= 6; ++r) {
-    int64_t n = r > 4 ? blocks / (2 * (r - 4)) : r > 0 && base > 0 ? r * slots / base : 1;
+    int64_t n = r > 4 ? blocks / (2 * (r - 4)) : r > 0 && base > 0 ? (full + r) * slots / base : 1;
     n = n < least ? least : n;
     n = n > blocks ? blocks : n;
     if (n < 1) n = 1;
@@ -726,7 +736,9 @@ size_t plan_decode(DecodeParams& p, int64_t keys) {
   const int64_t per = (blocks + best - 1) / best;              // blocks a split
   p.splits = (int32_t)(per > 0 ? (blocks + per - 1) / per : 1);
   p.keys_per_split = per * kKeys;
-  return p.splits > 1 ? (size_t)p.items * p.splits * p.rows * (kLatent * 2 + kPartFloats * 4) : 0;
+  if (p.splits == 1) return 0;
+  return (size_t)p.items * p.splits * p.rows * (kLatent * 2 + kPartFloats * 4) +
+         (dealt_out(p, paged) ? (p.items + 1) * sizeof(int32_t) : 0);
 }
 
 bool decode_fits(const DecodeParams& p) {
@@ -738,7 +750,10 @@ hipError_t launch_decode(DecodeParams p, bool fp4, bool paged, void* workspace,
   if (p.items == 0 || p.rows == 0) return hipSuccess;
   if (p.splits > 1) {
     p.part_o = static_cast<uint16_t*>(workspace);
-    p.part_ml = reinterpret_cast<float*>(p.part_o + (size_t)p.items * p.splits * p.rows * kLatent);
+    const size_t parts = (size_t)p.items * p.splits * p.rows;
+    p.part_ml = reinterpret_cast<float*>(p.part_o + parts * kLatent);
+    if (dealt_out(p, paged))
+      p.part_off = reinterpret_cast<int32_t*>(p.part_ml + parts * kPartFloats);
   }
   const hipError_t e = p.tile_rows == 128  ? launch_wide<4>(p, fp4, paged, stream)
                        : p.tile_rows == 64 ? launch_wide<2>(p, fp4, paged, stream)

@@ -66,13 +66,14 @@ struct DecodeParams {
   float* lse;               // [items][rows]
   // set by plan_decode and launch_decode
   int32_t tile_rows, row_tiles, splits;  // query rows a workgroup; their tiles
-  int64_t keys_per_split;   // a multiple of 32
-  uint16_t* part_o;         // [items][splits][rows][512] IEEE half, normalised and scaled
-  float* part_ml;           // [items][splits][rows][6]: maximum, sum, four scales
+  int64_t keys_per_split;   // a multiple of 32; at most, where part_off is there
+  uint16_t* part_o;         // [items * splits][rows][512] IEEE half, normalised and scaled
+  float* part_ml;           // [items * splits][rows][6]: maximum, sum, four scales
+  int32_t* part_off;        // or null, for fixed splits: [items + 1] the items' first parts
 };
 
 // Sets the launch shape for items of about `keys` keys; returns the workspace's bytes.
-size_t plan_decode(DecodeParams& p, int64_t keys);
+size_t plan_decode(DecodeParams& p, int64_t keys, bool paged);
 int64_t decode_grid(const DecodeParams& p);
 hipError_t launch_decode_narrow(const DecodeParams& p, bool fp4, bool paged, hipStream_t stream);
 // Whether a planned launch's grid is within the device's limits.

@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_narrow_kernel(DecodeParams
         p.lse[(int64_t)sh.item * p.rows + m] =
             l_run[i] == 0.f ? -INFINITY : (m_run[i] + log2f(l_run[i])) / kLog2e;
       } else {
-        const int64_t ps = ((int64_t)sh.item * p.splits + sh.split) * p.rows + m;
+        const int64_t ps = sh.part * p.rows + m;
         *reinterpret_cast<f32x2*>(p.part_ml + kPartFloats * ps) = f32x2{m_run[i], l_run[i]};
       }
     }
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_narrow_kernel(DecodeParams
     const float sum = l_run[rt];
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int64_t mrow = (int64_t)sh.item * p.rows + m;
-    const int64_t ps = ((int64_t)sh.item * p.splits + sh.split) * p.rows + m;
+    const int64_t ps = sh.part * p.rows + m;
     if (p.splits > 1 && sum == 0.f) continue;  // the merge does not read it
     float f = inv;
     if (p.splits > 1) {

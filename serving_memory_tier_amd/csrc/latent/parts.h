@@ -108,6 +108,19 @@ __device__ __forceinline__ f16x4 half4(float a, float b, float c, float d) {
   return f16x4{(_Float16)a, (_Float16)b, (_Float16)c, (_Float16)d};
 }
 
+// The sums of x over this lane and those before it; all 64 lanes take part.
+__device__ __forceinline__ int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);    // within 16 lanes:
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);    // 1, 2, 4, 8 lanes up
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);   // lane 15 to the next 16
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);   // lane 31 to the upper 32
+  return x;
+}
+
+__device__ __forceinline__ int lane_of(int x, int l) { return __builtin_amdgcn_readlane(x, l); }
+
 // The thread's number, opaque to the compiler: what it addresses with it is
 // computed where it is used instead of held in registers over the loop.
 __device__ __forceinline__ int fresh_tid() {

@@ -259,6 +259,25 @@ def test_paged_bounds_and_layers(fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("R,H,longest,bound_", [(1, 8, 900, 900), (3, 8, 700, 60000), (3, 130, 900, 60000),
+                                               (64, 5, 300, 3000), (64, 40, 200, 20000),
+                                               (65, 5, 300, 3000), (33, 64, 400, 401)])
+def test_paged_splits_follow_contexts(fmt, R, H, longest, bound_):
+    """Ragged contexts, none at all among them, under tight and loose bounds."""
+    import serving_memory_tier_amd as hs
+    rs = np.random.default_rng(R + H)
+    assert hs.hs_paged_mla_workspace_bytes(R, 1, H, bound_) > 0
+    page = 16
+    ctx = [longest] + [int(x) for x in rs.integers(0, longest, R - 1)]
+    if R > 2:
+        ctx[1], ctx[-1] = 0, 1
+    pages = -(-longest // page)
+    pool = make_pool(rs, (R * pages + 1) * page, fmt)
+    check_paged(pool, table(rs, R, pages, R * pages + 1), ctx, bits(rs, R, 1, H, 576), page, 0.05,
+                max_ctx=bound_)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("where", ["latent", "rope", "scale"])
 def test_paged_nan_rows(fmt, where):
     """A row with a NaN or an infinity makes the positions that see it NaN and leaves
