@@ -18,11 +18,11 @@
 // a row.
 //
 // Bound: the matrix cores, less what feeds them.  One request's 2,048 new tokens
-// on 8,192, 128 heads, FP8 rows: 1,540 us, 957 TFLOP/s, where a large matrix
+// on 8,192, 128 heads, FP8 rows: 1,536 us, 962 TFLOP/s, where a large matrix
 // product of the library reaches 1,210 to 1,330 (rows 7 us; expansion 341, of it
 // 537 MB written; attention 1,300, 925 TFLOP/s, 43 % of a loop of MFMAs
-// alone).  Four requests of up to 753 on 4,849, 64 heads, 4-bit rows: 755 us.
-// Three of up to 130 on 500, 16 heads: 34 us, three dependent launches.
+// alone).  Four requests of up to 753 on 4,849, 64 heads, 4-bit rows: 740 us.
+// Three of up to 130 on 500, 16 heads: 33.5 us, three dependent launches.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -356,7 +356,10 @@ __global__ void __launch_bounds__(64 * NW, 2) prefill_attend_kernel(PrefillParam
   {
     const uint16_t* q = p.q + (qrow * p.heads + head) * kQ;
 #pragma unroll
-    for (int ks = 0; ks < 12; ++ks) qb[ks] = *reinterpret_cast<const bf16x8*>(q + 16 * ks + 8 * hi);
+    for (int ks = 0; ks < 12; ++ks)
+      qb[ks] = __builtin_bit_cast(
+          bf16x8,
+          *reinterpret_cast<const u32x4*>(q + 16 * ks + 8 * hi) ^ (p.scale < 0.f ? 0x80008000u : 0u));
   }
   f32x16 o[4];
 #pragma unroll
@@ -364,7 +367,9 @@ __global__ void __launch_bounds__(64 * NW, 2) prefill_attend_kernel(PrefillParam
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
   float m_run = -INFINITY, l_run = 0.f;
-  const float qk_scale = p.scale * kLog2e;
+  // scores stay as the products give them and are scaled in the exponent; so the
+  // scale has to be positive (a negative one turns the queries' signs instead)
+  const float qk_scale = fmaxf(fabsf(p.scale) * kLog2e, 1e-38f);
   const int64_t at = p.off[r];
   const uint8_t* hkv =
       reinterpret_cast<const uint8_t*>(p.heads_kv + ((int64_t)head * p.num_kv + at) * kHeadRow);
@@ -408,8 +413,6 @@ __global__ void __launch_bounds__(64 * NW, 2) prefill_attend_kernel(PrefillParam
                                              16 * ((2 * ks + hi) ^ ((row >> 1) & 7))),
             qb[8 + ks], sc[kt], 0, 0, 0);
     }
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt) sc[kt] *= qk_scale;
     // ---- masks: keys without a row, keys past the query
     const uint64_t gone = __ballot(flag == 1), bad = __ballot(flag == 2);
     if (gone != 0 || bad != 0 || k0 + kTile > least) {
@@ -432,18 +435,19 @@ __global__ void __launch_bounds__(64 * NW, 2) prefill_attend_kernel(PrefillParam
     float mb = sc[0][0];
 #pragma unroll
     for (int i = 1; i < 32; ++i) mb = fmaxf(mb, sc[i / 16][i % 16]);
-    mb = fmaxf(mb, __shfl_xor(mb, 32));
+    mb = max_halves(mb) * qk_scale;
     const bool grow = mb > m_run + kStaleMax;
     const float m_new = grow ? mb : m_run;
     const float alpha = grow ? __builtin_amdgcn_exp2f(m_run - m_new) : 1.f;
     const float base = m_new == -INFINITY ? 0.f : m_new;
-    float ls = 0.f;
+    float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      sc[i / 16][i % 16] = __builtin_amdgcn_exp2f(sc[i / 16][i % 16] - base);
-      ls += sc[i / 16][i % 16];
+      sc[i / 16][i % 16] =
+          __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i / 16][i % 16], qk_scale, -base));
+      ls[i % 4] += sc[i / 16][i % 16];
     }
-    l_run = l_run * alpha + ls;
+    l_run = l_run * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
     m_run = m_new;
     if (__any(grow)) {
 #pragma unroll

@@ -359,6 +359,20 @@ def test_values_past_the_range_of_a_later_token():
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("H", [16, 32, 64, 128])
+def test_scales_of_any_sign(fmt, H):
+    """A negative scale is the positive one with the queries negated, bit for bit; a
+    zero one averages the values seen."""
+    rs = np.random.default_rng(H)
+    pool, ctx = make_pool(rs, 40 * 16, fmt), [300, 90]
+    bt, q = table(rs, 2, 19, 40), bits(rs, 2, 1, H, 576)
+    plus = run_paged(pool, bt, ctx, q, 16, 0.07)
+    minus = run_paged(pool, bt, ctx, q ^ np.uint16(0x8000), 16, -0.07)
+    assert (plus[0] == minus[0]).all() and (plus[1] == minus[1]).all()
+    check_paged(pool, bt, ctx, q, 16, 0.0)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_offsets_past_32_bits(fmt):
     """Rows past the fourth gibibyte of a layer."""
     import serving_memory_tier_amd as hs

@@ -237,3 +237,18 @@ def test_split_outputs_keep_their_range(fmt, power):
     bt = table(rs, 1, 24, 24)
     got = run(pool, bt, ctx, start, q, w, page, 0.05)
     check(got, pool, bt, ctx, start, q, w, page, 0.05, floor=2.0 ** (power - 30))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_scales_of_any_sign(fmt):
+    """A negative scale is the positive one with the queries negated, bit for bit; a
+    zero one averages the values seen."""
+    rs = np.random.default_rng(9)
+    page, ctx, start, H = 16, [300, 90], [0, 150, 240], 3
+    pool = make_pool(rs, 40 * page, fmt)
+    bt = table(rs, 2, 19, 40, holes=0.1)
+    q, w = bits(rs, 240, H, 192), bits(rs, H, 256, 512, mult=0.05)
+    plus = run(pool, bt, ctx, start, q, w, page, 0.07)
+    minus = run(pool, bt, ctx, start, q ^ np.uint16(0x8000), w, page, -0.07)
+    assert (plus == minus).all()
+    check(run(pool, bt, ctx, start, q, w, page, 0.0), pool, bt, ctx, start, q, w, page, 0.0)
