@@ -94,13 +94,15 @@ __device__ __forceinline__ void mask(const Lists<32 * NP>& s, const Share& sh, i
   }
 }
 
-// One block of the online softmax: scores (in log2 units) to probabilities.
-// The maximum is renewed, and the output rescaled, only when it grows by 2^8.
-__device__ __forceinline__ void softmax(f32x16& sc, float& m_run, float& l_run, f32x16 (&o)[8]) {
+// One block of the online softmax: scores, which qk_scale > 0 brings to log2
+// units, to probabilities.  The maximum is renewed, and the output rescaled, only
+// when it grows by 2^8.
+__device__ __forceinline__ void softmax(f32x16& sc, float qk_scale, float& m_run, float& l_run,
+                                        f32x16 (&o)[8]) {
   float mb = sc[0];
 #pragma unroll
   for (int i = 1; i < 16; ++i) mb = fmaxf(mb, sc[i]);
-  mb = max_halves(mb);
+  mb = max_halves(mb) * qk_scale;
   const bool grow = mb > m_run + kStaleMax;
   const float m_new = grow ? mb : m_run;
   const float alpha = grow ? __builtin_amdgcn_exp2f(m_run - m_new) : 1.f;
@@ -108,7 +110,7 @@ __device__ __forceinline__ void softmax(f32x16& sc, float& m_run, float& l_run, 
   float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    sc[i] = __builtin_amdgcn_exp2f(sc[i] - base);
+    sc[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], qk_scale, -base));
     ls[i % 4] += sc[i];
   }
   l_run = l_run * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(128 * NP) decode_fp4_kernel(DecodeParams p) {
     for (int ks = 0; ks < 18; ++ks) {
       const int at = ks < 16 ? half * 256 + ks * 16 + 8 * hi
                              : kLatent + half * 32 + (ks - 16) * 16 + 8 * hi;
-      const bf16x8 v = *reinterpret_cast<const bf16x8*>(q + at);
+      const bf16x8 v = signed_query(q + at, p.scale);
       if (ks < kQueryRegs)
         qb[ks] = v;
       else
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(128 * NP) decode_fp4_kernel(DecodeParams p) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
   float m_run = -INFINITY, l_run = 0.f;        // l_run: this lane's keys only
-  const float qk_scale = p.scale * kLog2e;
+  const float qk_scale = positive_scale(p.scale);
   if (blocks > 0) {
     f.store(s.blk[0], ids, PAGED && kKeys > sh.edge, sh.edge);
     if (blocks > 1) {
@@ -387,11 +389,11 @@ __global__ void __launch_bounds__(128 * NP) decode_fp4_kernel(DecodeParams p) {
     for (int i = 0; i < 4; ++i) {
       const f32x4 v = s.xs[other][i][l];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sc[4 * i + j] = (sc[4 * i + j] + v[j]) * qk_scale;
+      for (int j = 0; j < 4; ++j) sc[4 * i + j] += v[j];
     }
     if (!late) next();
     mask<PAGED, NP>(s.lists, sh, bi, duo * 32 + col, hi, sc);
-    softmax(sc, m_run, l_run, o);
+    softmax(sc, qk_scale, m_run, l_run, o);
     // ---- O^T += V^T P^T.  Step ks covers keys 16 ks + 4 hi + {0..3, 8..11},
     // the ones this lane holds; lane c of a 16-lane group supplies row c / 4
     // and 4 dimensions of each transposing read
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__(128 * NP) decode_fp8_kernel(DecodeParams p) {
     for (int ks = 0; ks < 18; ++ks) {
       const int at = ks < 16 ? half * 256 + (ks / 2) * 32 + 16 * hi + 8 * (ks % 2)
                              : kLatent + half * 32 + (ks - 16) * 16 + 8 * hi;
-      const bf16x8 v = *reinterpret_cast<const bf16x8*>(q + at);
+      const bf16x8 v = signed_query(q + at, p.scale);
       if (ks < 18 - kQuerySteps8)
         qb[ks] = v;
       else
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__(128 * NP) decode_fp8_kernel(DecodeParams p) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
   float m_run = -INFINITY, l_run = 0.f;        // l_run: this lane's keys only
-  const float qk_scale = p.scale * kLog2e;
+  const float qk_scale = positive_scale(p.scale);
   wait_rows();
   if (blocks > 0 && kKeys > sh.edge) sanitize_rows<false, T>(s.blk[0], s.lists.ids, sh.edge);
   __syncthreads();
@@ -557,10 +559,10 @@ __global__ void __launch_bounds__(128 * NP) decode_fp8_kernel(DecodeParams p) {
     for (int i = 0; i < 4; ++i) {
       const f32x4 v = s.xs[other][i][l];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sc[4 * i + j] = (sc[4 * i + j] + v[j]) * qk_scale;
+      for (int j = 0; j < 4; ++j) sc[4 * i + j] += v[j];
     }
     mask<true, NP>(s.lists, sh, bi, duo * 32 + col, hi, sc);
-    softmax(sc, m_run, l_run, o);
+    softmax(sc, qk_scale, m_run, l_run, o);
     // ---- O^T += V^T P'^T, P' = p * scale of the latent tile.  Step ks covers
     // keys 16 ks + 4 hi + {0..3, 8..11}, the ones this lane holds; lane c of a
     // 16-lane group supplies row c / 2 of those and 8 dimensions

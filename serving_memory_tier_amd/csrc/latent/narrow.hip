@@ -49,15 +49,16 @@ __device__ __forceinline__ void mask8(const Lists<ROWS>& s, const Share& sh, int
   }
 }
 
-// One block of the online softmax of a lane's 8 keys: scores (in log2 units) to
-// probabilities.  The maximum is renewed, and the output to be rescaled by the
+// One block of the online softmax of a lane's 8 keys: scores, which qk_scale > 0
+// brings to log2 units, to probabilities.  The maximum is renewed, and the output to be rescaled by the
 // returned factor, only when it grows by 2^8.
-__device__ __forceinline__ float softmax8(float (&sc)[8], float& m_run, float& l_run) {
+__device__ __forceinline__ float softmax8(float (&sc)[8], float qk_scale, float& m_run,
+                                         float& l_run) {
   float mb = sc[0];
 #pragma unroll
   for (int i = 1; i < 8; ++i) mb = fmaxf(mb, sc[i]);
   mb = fmaxf(mb, __shfl_xor(mb, 16));
-  mb = fmaxf(mb, __shfl_xor(mb, 32));
+  mb = fmaxf(mb, __shfl_xor(mb, 32)) * qk_scale;
   const bool grow = mb > m_run + kStaleMax;
   const float m_new = grow ? mb : m_run;
   const float alpha = grow ? __builtin_amdgcn_exp2f(m_run - m_new) : 1.f;
@@ -65,7 +66,7 @@ __device__ __forceinline__ float softmax8(float (&sc)[8], float& m_run, float& l
   float ls = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    sc[i] = __builtin_amdgcn_exp2f(sc[i] - base);
+    sc[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], qk_scale, -base));
     ls += sc[i];
   }
   l_run = l_run * alpha + ls;
@@ -111,9 +112,9 @@ __global__ void __launch_bounds__(kThreads, 2) decode_narrow_kernel(DecodeParams
       const uint16_t* q = p.q + ((int64_t)sh.item * p.rows + m) * kDim;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        qb[rt][i] = *reinterpret_cast<const bf16x8*>(
-            q + 128 * w + (FP4 ? 32 * g + 8 * i : 64 * (i / 2) + 16 * g + 8 * (i % 2)));
-      qb[rt][4] = *reinterpret_cast<const bf16x8*>(q + kLatent + 32 * (w & 1) + 8 * g);
+        qb[rt][i] = signed_query(
+            q + 128 * w + (FP4 ? 32 * g + 8 * i : 64 * (i / 2) + 16 * g + 8 * (i % 2)), p.scale);
+      qb[rt][4] = signed_query(q + kLatent + 32 * (w & 1) + 8 * g, p.scale);
     }
   }
   // O^T of the wave's dimensions, by column (row of the tile): tile dt's rows are
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_narrow_kernel(DecodeParams
     m_run[i] = -INFINITY;
     l_run[i] = 0.f;
   }
-  const float qk_scale = p.scale * kLog2e;
+  const float qk_scale = positive_scale(p.scale);
   int cur = 0;                                 // bi modulo the buffers
   for (int bi = 0; bi < blocks; ++bi) {
     uint8_t* raw = s.raw[cur];
@@ -209,10 +210,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_narrow_kernel(DecodeParams
         for (int v = 0; v < kWaves; ++v)
           sum += s.xs[v][i][mt][l];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[i][4 * mt + r] = sum[r] * qk_scale;
+        for (int r = 0; r < 4; ++r) x[i][4 * mt + r] = sum[r];
       }
       mask8<PAGED, 16 * RT>(s.lists, sh, bi, 16 * i + col, g, x[i]);
-      const float alpha = softmax8(x[i], m_run[i], l_run[i]);
+      const float alpha = softmax8(x[i], qk_scale, m_run[i], l_run[i]);
       if (__any(alpha != 1.f)) {
 #pragma unroll
         for (int dt = 0; dt < 8; ++dt) o[i][dt] *= alpha;

@@ -97,6 +97,19 @@ __device__ __forceinline__ float max_halves(float x) {
   return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
 }
 
+// Scores stay as the products give them and are scaled in the exponent, so the
+// scale has to be positive: a negative one turns the queries' signs instead, zero
+// becomes the least that keeps a masked score -infinity.
+__device__ __forceinline__ float positive_scale(float scale) {
+  const float s = fmaxf(fabsf(scale) * kLog2e, 1e-38f);
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, s)));
+}
+
+__device__ __forceinline__ bf16x8 signed_query(const uint16_t* q, float scale) {
+  return __builtin_bit_cast(
+      bf16x8, *reinterpret_cast<const u32x4*>(q) ^ (scale < 0.f ? 0x80008000u : 0u));
+}
+
 // The power of two (its exponent) that brings values of magnitude `most` at the
 // largest to [1, 2), where half precision keeps 11 bits of them.
 __device__ __forceinline__ int half_exponent(float most) {

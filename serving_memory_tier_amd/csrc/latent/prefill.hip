@@ -357,9 +357,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prefill_attend_kernel(PrefillParam
     const uint16_t* q = p.q + (qrow * p.heads + head) * kQ;
 #pragma unroll
     for (int ks = 0; ks < 12; ++ks)
-      qb[ks] = __builtin_bit_cast(
-          bf16x8,
-          *reinterpret_cast<const u32x4*>(q + 16 * ks + 8 * hi) ^ (p.scale < 0.f ? 0x80008000u : 0u));
+      qb[ks] = signed_query(q + 16 * ks + 8 * hi, p.scale);
   }
   f32x16 o[4];
 #pragma unroll
@@ -367,9 +365,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prefill_attend_kernel(PrefillParam
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
   float m_run = -INFINITY, l_run = 0.f;
-  // scores stay as the products give them and are scaled in the exponent; so the
-  // scale has to be positive (a negative one turns the queries' signs instead)
-  const float qk_scale = fmaxf(fabsf(p.scale) * kLog2e, 1e-38f);
+  const float qk_scale = positive_scale(p.scale);
   const int64_t at = p.off[r];
   const uint8_t* hkv =
       reinterpret_cast<const uint8_t*>(p.heads_kv + ((int64_t)head * p.num_kv + at) * kHeadRow);
