@@ -40,13 +40,13 @@
 // Bound: a block's LDS reads (18 KB of keys and 16 KB of values a wave, the
 // transposing reads at half the rate of the others), its MFMAs and the steps
 // between them, which two waves a SIMD overlap in part (no LDS bank conflict is
-// left over 4-bit rows).  512 tokens x 128 heads x 2,048 4-bit rows: 353 us, 811
-// TFLOP/s, 37 % of what a loop of these MFMAs alone reaches (2,170); a large matrix
-// product of the library reaches 1,210 to 1,330.  32 x 128 x 2,048 takes 45 us, of it the
-// merge 8 (eight splits, 34 MB written and read); 8 requests x 4 positions x 128
-// heads on up to 74,160 4-bit tokens 799 us (633 TFLOP/s; its splits fill 3.6
-// rounds of the chip and take 4); 32 x 128 heads on up to 8,192 FP8 tokens
-// 114 us (484 TFLOP/s: the conversions at use).
+// left over 4-bit rows).  512 tokens x 128 heads x 2,048 4-bit rows: 338 us, 846
+// TFLOP/s, 39 % of what a loop of these MFMAs alone reaches (2,170); a large matrix
+// product of the library reaches 1,210 to 1,330.  32 x 128 x 2,048 takes 45 us, of
+// it the merge 8 (eight splits, 34 MB written and read); 8 requests x 4 positions x
+// 128 heads on half to all of 74,160 4-bit tokens 637 us (794 TFLOP/s); 32 x 128
+// heads on half to all of 8,192 FP8 tokens 100 us (551 TFLOP/s: the conversions at
+// use).
 //
 // Rounding: scores, softmax and outputs in float32; the probabilities times
 // the FP8 scales are rounded to bfloat16 for the MFMAs (half steps of 2^-8 that
@@ -699,7 +699,7 @@ static bool dealt_out(const DecodeParams& p, bool paged) {
 size_t plan_decode(DecodeParams& p, int64_t keys, bool paged) {
   // The least tile that holds the rows: up to 32 the narrow kernel, up to 64 this
   // file's with two wave pairs.  Measured with tiles of 16, 32, 64 and 128 rows, 32
-  // requests on up to 8,192 FP8 tokens: 16 heads 47, 59, 99 and 107 us; 32 heads
+  // requests on up to 8,192 FP8 tokens (splits by the bound): 16 heads 47, 59, 99 and 107 us; 32 heads
   // 79, 63, 101 and 111; 64 heads 146, 109, 106 and 117; 128 heads 277, 202, 193
   // and 125
   p.tile_rows = p.rows <= 16 ? 16 : p.rows <= 32 ? 32 : p.rows <= 64 ? 64 : 128;

@@ -14,12 +14,11 @@
 // Rows go from the pool into LDS as they are and are converted at use, exactly;
 // two barriers a block (rows complete; shares complete), two workgroups a unit.
 //
-// Bound: with enough requests the rows' bytes (32 requests x 16 heads on up to
-// 8,192 FP8 tokens, 129 MB: 46 us with the merge, 2.8 TB/s over all, over 5 TB/s
-// while all workgroups run; 4-bit rows 48 us, 32 heads 62 and 66 us, bound by the
-// conversions and the softmax that four waves repeat); with few requests a
-// block's chain of barriers, LDS and MFMAs, 1.5 us: 3 requests x 16 heads on up to
-// 500 tokens 12.7 us, of it the merge 4.
+// Bound: with enough requests the rows' bytes (32 requests x 16 heads on half to
+// all of 8,192 FP8 tokens, 129 MB: 43 us with the merge, 3.0 TB/s over all; 4-bit
+// rows 44 us, 32 heads 58 and 59 us, bound by the conversions and the softmax that
+// four waves repeat); with few requests a block's chain of barriers, LDS and MFMAs,
+// 1.5 us: 3 requests x 16 heads on up to 500 tokens 13.3 us, of it the merge 4.8.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -18,9 +18,9 @@
 // a row.
 //
 // Bound: the matrix cores, less what feeds them.  One request's 2,048 new tokens
-// on 8,192, 128 heads, FP8 rows: 1,536 us, 962 TFLOP/s, where a large matrix
+// on 8,192, 128 heads, FP8 rows: 1,525 us, 969 TFLOP/s, where a large matrix
 // product of the library reaches 1,210 to 1,330 (rows 7 us; expansion 341, of it
-// 537 MB written; attention 1,300, 925 TFLOP/s, 43 % of a loop of MFMAs
+// 537 MB written; attention 1,215 to 1,300, 925 TFLOP/s, 43 % of a loop of MFMAs
 // alone).  Four requests of up to 753 on 4,849, 64 heads, 4-bit rows: 740 us.
 // Three of up to 130 on 500, 16 heads: 33.5 us, three dependent launches.
 
