@@ -481,7 +481,8 @@ hs_status hs_mla_append(const hs_layout* layout, const hs_batch* batch, int32_t 
  * bytes, 16-byte aligned (may be NULL when that is 0), overwritten; calls
  * sharing one must not overlap.
  * Errors: HS_ERR_INVALID_ARGUMENT (null or misaligned pointers with work to
- * do, a short workspace, num_heads < 1, negative sizes, bad layout),
+ * do, a short workspace, num_heads < 1, negative sizes, a scale that is not
+ * finite, bad layout),
  * HS_ERR_UNSUPPORTED (another row_bytes, over 1,048,576 tokens, heads or
  * top_k, a launch of 2^32 threads), HS_ERR_LAUNCH.
  */
@@ -519,9 +520,9 @@ size_t hs_sparse_mla_fp4_workspace_bytes(int32_t num_tokens, int32_t num_heads, 
  * sharing one must not overlap.
  * Precision: as hs_sparse_mla_decode_fp4 (FP8 scales are applied in float32).
  * Errors: HS_ERR_INVALID_ARGUMENT (null or misaligned pointers with work to
- * do, a short workspace, num_pos or num_heads < 1, a negative max_ctx, a bad
- * layer or layout), HS_ERR_UNSUPPORTED (another row_bytes, P * H over
- * 1,048,576, a launch of 2^32 threads), HS_ERR_LAUNCH.
+ * do, a short workspace, num_pos or num_heads < 1, a negative max_ctx, a scale
+ * that is not finite, a bad layer or layout), HS_ERR_UNSUPPORTED (another
+ * row_bytes, P * H over 1,048,576, a launch of 2^32 threads), HS_ERR_LAUNCH.
  */
 hs_status hs_paged_mla_decode(const hs_layout* layout, const hs_batch* batch, int32_t layer,
                               const uint16_t* q, int32_t num_pos, int32_t num_heads,
@@ -560,9 +561,10 @@ size_t hs_paged_mla_workspace_bytes(int32_t num_reqs, int32_t num_pos, int32_t n
  * and out are rounded to bfloat16, key splits' outputs to scaled half precision
  * before their merge in float32.  The expanded values have to be within the range of float32.
  * Errors: HS_ERR_INVALID_ARGUMENT (null or misaligned pointers with work to
- * do, a short workspace, negative sizes, num_heads < 1, a bad layer or
- * layout), HS_ERR_UNSUPPORTED (another row_bytes, over 1,048,576 heads or
- * requests, over 65,535 tiles of 128 tokens or queries), HS_ERR_LAUNCH.
+ * do, a short workspace, negative sizes, num_heads < 1, a scale that is not
+ * finite, a bad layer or layout), HS_ERR_UNSUPPORTED (another row_bytes, over
+ * 1,048,576 heads or requests, over 65,535 tiles of 128 tokens or queries),
+ * HS_ERR_LAUNCH.
  */
 hs_status hs_mla_prefill(const hs_layout* layout, const hs_batch* batch, int32_t layer,
                          const int32_t* q_start, int32_t num_q, int32_t num_kv, const uint16_t* q,

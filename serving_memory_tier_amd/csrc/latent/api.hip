@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "hisparse.h"
 #include "hs_check.h"
 #include "latent.h"
@@ -117,7 +119,8 @@ hs_status hs_sparse_mla_decode_fp4(const hs_layout* layout, const uint8_t* kv_la
   hs_status s = check_layout(layout);
   if (s != HS_OK) return s;
   if (layout->row_bytes != HS_ROW_FP4) return HS_ERR_UNSUPPORTED;
-  if (num_tokens < 0 || top_k < 0 || num_heads < 1) return HS_ERR_INVALID_ARGUMENT;
+  if (num_tokens < 0 || top_k < 0 || num_heads < 1 || !std::isfinite(sm_scale))
+    return HS_ERR_INVALID_ARGUMENT;
   if (num_tokens > kMaxRows || top_k > kMaxRows || num_heads > kMaxRows) return HS_ERR_UNSUPPORTED;
   if (num_tokens == 0) return HS_OK;
   if (top_k > 0 && (!kv_layer || !row_ids || !aligned16(kv_layer))) return HS_ERR_INVALID_ARGUMENT;
@@ -154,7 +157,8 @@ hs_status hs_paged_mla_decode(const hs_layout* layout, const hs_batch* batch, in
   if (!batch || layer < 0 || layer >= layout->num_layers) return HS_ERR_INVALID_ARGUMENT;
   bool fp4 = false;
   if ((s = row_format(layout, &fp4)) != HS_OK) return s;
-  if (batch->num_reqs < 0 || batch->max_pages < 1 || num_pos < 1 || num_heads < 1 || max_ctx < 0)
+  if (batch->num_reqs < 0 || batch->max_pages < 1 || num_pos < 1 || num_heads < 1 || max_ctx < 0 ||
+      !std::isfinite(sm_scale))
     return HS_ERR_INVALID_ARGUMENT;
   if ((int64_t)num_pos * num_heads > kMaxRows) return HS_ERR_UNSUPPORTED;
   if (batch->num_reqs == 0) return HS_OK;
@@ -203,7 +207,8 @@ hs_status hs_mla_prefill(const hs_layout* layout, const hs_batch* batch, int32_t
   if (!batch || layer < 0 || layer >= layout->num_layers) return HS_ERR_INVALID_ARGUMENT;
   bool fp4 = false;
   if ((s = row_format(layout, &fp4)) != HS_OK) return s;
-  if (batch->num_reqs < 0 || batch->max_pages < 1 || num_q < 0 || num_kv < 0 || num_heads < 1)
+  if (batch->num_reqs < 0 || batch->max_pages < 1 || num_q < 0 || num_kv < 0 || num_heads < 1 ||
+      !std::isfinite(sm_scale))
     return HS_ERR_INVALID_ARGUMENT;
   if (num_heads > kMaxRows || batch->num_reqs > kMaxRows) return HS_ERR_UNSUPPORTED;
   if (batch->num_reqs == 0 || num_q == 0) return HS_OK;

@@ -273,3 +273,15 @@ def test_bindings_refuse_wrong_tensors():
         prefill(workspace=t(64, dtype=u8))
     with pytest.raises(hs.HsError):
         prefill(stream=0)
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), float("-inf")])
+def test_scales_that_are_not_finite(lib, scale):
+    r = ctypes.byref
+    l8, l4, b = layout(), layout(row_bytes=400), batch(ctx_len=FAKE)
+    assert lib.hs_sparse_mla_decode_fp4(r(l4), FAKE, FAKE, 1, 8, FAKE, 1, scale, FAKE, FAKE, FAKE,
+                                        BIG, None) == 1
+    assert lib.hs_paged_mla_decode(r(l8), r(b), 0, FAKE, 1, 1, 8, scale, FAKE, FAKE, FAKE, BIG,
+                                   None) == 1
+    assert lib.hs_mla_prefill(r(l8), r(b), 0, FAKE, 1, 8, FAKE, 1, FAKE, scale, FAKE, FAKE, BIG,
+                              None) == 1
