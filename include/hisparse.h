@@ -513,8 +513,8 @@ size_t hs_sparse_mla_fp4_workspace_bytes(int32_t num_tokens, int32_t num_heads, 
  * Arguments: q device bf16 [R][P][H][576]; out device bf16 [R][P][H][512];
  * lse device float [R][P][H]; q and out 16-byte aligned; max_ctx: no smaller
  * than any ctx_len[r] (tokens from max_ctx on are not attended to), and may be
- * far larger, as in a captured call: up to 64 requests' work is split by their
- * contexts, more by max_ctx.  Uses batch->num_reqs, max_pages, block_table, ctx_len and
+ * far larger, as in a captured call: up to 512 requests' work is split by
+ * their contexts, more by max_ctx.  Uses batch->num_reqs, max_pages, block_table, ctx_len and
  * kv_pool.  workspace: at least hs_paged_mla_workspace_bytes(R, P, H, max_ctx)
  * bytes, 16-byte aligned (may be NULL when that is 0), overwritten; calls
  * sharing one must not overlap.

@@ -44,7 +44,7 @@
 // TFLOP/s, 39 % of what a loop of these MFMAs alone reaches (2,170); a large matrix
 // product of the library reaches 1,210 to 1,330.  32 x 128 x 2,048 takes 45 us, of
 // it the merge 8 (eight splits, 34 MB written and read); 8 requests x 4 positions x
-// 128 heads on half to all of 74,160 4-bit tokens 637 us (794 TFLOP/s); 32 x 128
+// 128 heads on half to all of 74,160 4-bit tokens 625 us (810 TFLOP/s); 32 x 128
 // heads on half to all of 8,192 FP8 tokens 100 us (551 TFLOP/s: the conversions at
 // use).
 //
@@ -690,10 +690,10 @@ int64_t decode_grid(const DecodeParams& p) {
   return ((int64_t)p.items * p.splits + 7) / 8 * 8 * p.row_tiles;
 }
 
-// Whether the kernel deals out the splits by the contexts: a wave's lanes a request
-// each, and splits of more than the least, one block.
+// Whether the kernel deals out the splits by the contexts: where they are of more
+// than the least, one block.
 static bool dealt_out(const DecodeParams& p, bool paged) {
-  return paged && p.items <= 64 && p.splits > 1 && p.keys_per_split > kKeys;
+  return paged && p.items <= kDealtReqs && p.splits > 1 && p.keys_per_split > kKeys;
 }
 
 size_t plan_decode(DecodeParams& p, int64_t keys, bool paged) {
@@ -713,6 +713,7 @@ size_t plan_decode(DecodeParams& p, int64_t keys, bool paged) {
   const int64_t base = (int64_t)p.items * p.row_tiles;
   const int64_t blocks = (keys + kKeys - 1) / kKeys;
   const int64_t slots = p.tile_rows >= 64 ? 256 : 512;
+  p.round = (int32_t)(slots / p.row_tiles > 0 ? slots / p.row_tiles : 1);
   const int64_t least = (blocks * kKeys + kDecodeSplitKeys - 1) / kDecodeSplitKeys;
   int64_t best = 1;
   double best_t = 1e300;

@@ -33,36 +33,75 @@ struct Share {
   int n, edge;                               // the first query row sees the fewest keys, `edge`
 };
 
-// The paged form's splits for up to 64 requests.  The launch has items * splits
-// places, enough for contexts of the caller's bound; here, where the contexts are
-// known, they are dealt out anew: the fewest blocks a split with which the
-// requests' splits, one at least each, fit the places.  So ragged contexts keep
+// The paged form's splits for up to kDealtReqs requests.  The launch has items *
+// splits places, enough for contexts of the caller's bound; here, where the
+// contexts are known, they are dealt out anew: of the rounds of the chip that the
+// longest splits would take, the last is filled, and a split is the fewest blocks
+// with which the requests' splits, one at least each, fit.  So ragged contexts keep
 // the chip as full as equal ones, and a bound far above the contexts (a captured
-// call's) costs nothing.  Against splits fixed by the bound: 8 requests x 4 x 128
-// heads on half to all of 74,160 4-bit tokens 638 us, 799 before; 32 x 128 on
-// half to all of 8,192 FP8 tokens 101 and 114; 32 x 16 heads 43 and 47; its cost
-// 0.6 us.  Place -> item, split; false past the last.
+// call's) costs little.  Against splits fixed by the bound: 8 requests x 4 x 128
+// heads on half to all of 74,160 4-bit tokens 625 us, 799 before; 32 x 128 on half
+// to all of 8,192 FP8 tokens 101 and 114; 32 x 16 heads 43 and 47; at its cost 0.6
+// us.  Under a bound of 74,160, on half to all of 2,000 FP8 tokens: 64 x 128 heads
+// 87 us, 168 with every place filled; 128 x 16 heads 53, 119 with fixed splits; 300
+// x 128 heads on 500 201 and 631.  Place -> item, split; false past the last.
 __device__ __forceinline__ bool place(const DecodeParams& p, int32_t pair, bool first, int32_t& item,
                                       int32_t& split, int64_t& per) {
-  const int l = threadIdx.x & 63, slots = p.items * p.splits;
-  int b = 0;                                 // lane l's request's blocks
-  if (l < p.items)
-    b = (int)((min((int64_t)max(p.ctx_len[l], 0), (int64_t)p.max_keys) + kKeys - 1) / kKeys);
-  auto ends = [&](int n) { return wave_scan(l < p.items ? max(1, (b + n - 1) / n) : 0); };
+  constexpr int kEach = kDealtReqs / 64;     // requests a lane, at most
+  const int l = threadIdx.x & 63, slots = p.items * p.splits, each = (p.items + 63) / 64;
+  int b[kEach];                              // blocks of request l * each + i, -1 past the last
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int r = l * each + i;
+    b[i] = -1;
+    if (i < each && r < p.items) {
+      b[i] = (int)((min((int64_t)max(p.ctx_len[r], 0), (int64_t)p.max_keys) + kKeys - 1) / kKeys);
+      sum += b[i];
+    }
+  }
+  auto parts = [&](int blocks, int n) { return blocks < 0 ? 0 : max(1, (blocks + n - 1) / n); };
+  auto mine = [&](int n) {                   // this lane's requests' splits of n blocks
+    int x = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (i < each) x += parts(b[i], n);
+    return x;
+  };
+  int hi = (int)(p.keys_per_split / kKeys);
+  const int least = lane_of(wave_scan(mine(hi)), 63);
+  const int use = min(slots, (least + p.round - 1) / p.round * p.round);
+  if (pair >= use) return false;             // a loose bound's many, soonest
   // n blocks a split make at most all / n + items of them
-  const int all = lane_of(wave_scan(b), 63);
-  int lo = max(1, (all + slots - 1) / slots);
-  int hi = min((int)(p.keys_per_split / kKeys), all / (slots - p.items) + 1);
+  const int all = lane_of(wave_scan(sum), 63);
+  int lo = max(1, (all + use - 1) / use);
+  if (use > p.items) hi = min(hi, all / (use - p.items) + 1);
   while (lo < hi) {
     const int mid = (lo + hi) / 2;
-    if (lane_of(ends(mid), 63) <= slots) hi = mid; else lo = mid + 1;
+    if (lane_of(wave_scan(mine(mid)), 63) <= use) hi = mid; else lo = mid + 1;
   }
-  const int end = ends(lo);
-  if (first && threadIdx.x < p.items) p.part_off[l + 1] = end;
-  if (first && threadIdx.x == 0) p.part_off[0] = 0;
-  if (pair >= lane_of(end, 63)) return false;
-  item = __popcll(__ballot(l < p.items && end <= pair));
-  split = pair - (item > 0 ? lane_of(end, item - 1) : 0);
+  const int own = mine(lo), end = wave_scan(own), total = lane_of(end, 63);
+  if (first && threadIdx.x < 64) {
+    int at = end - own;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (b[i] < 0) continue;
+      p.part_off[l * each + i] = at;
+      at += parts(b[i], lo);
+    }
+    if (l == 0) p.part_off[p.items] = total;
+  }
+  if (pair >= total) return false;
+  const int lane = __popcll(__ballot(end <= pair));
+  int rest = pair - (lane > 0 ? lane_of(end, lane - 1) : 0);
+  item = -1;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (i >= each || item >= 0) continue;
+    const int n = parts(lane_of(b[i], lane), lo);
+    if (rest < n) item = lane * each + i; else rest -= n;
+  }
+  split = rest;
   per = (int64_t)lo * kKeys;
   return true;
 }

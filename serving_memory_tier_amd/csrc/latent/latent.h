@@ -47,6 +47,8 @@ hipError_t launch_append(AppendParams p, bool fp4, bool interleaved, hipStream_t
 // the item's keys; 512-wide bfloat16 outputs.
 constexpr int kDecodeSplitKeys = 2048;     // keys a split, at most: their row ids are in LDS
 
+constexpr int kDealtReqs = 512;           // requests whose splits the kernel deals out
+
 struct DecodeParams {
   const uint8_t* kv;        // one layer of the pool
   int64_t pool_rows;
@@ -66,6 +68,7 @@ struct DecodeParams {
   float* lse;               // [items][rows]
   // set by plan_decode and launch_decode
   int32_t tile_rows, row_tiles, splits;  // query rows a workgroup; their tiles
+  int32_t round;            // (item, split) places that the chip runs at once
   int64_t keys_per_split;   // a multiple of 32; at most, where part_off is there
   uint16_t* part_o;         // [items * splits][rows][512] IEEE half, normalised and scaled
   float* part_ml;           // [items * splits][rows][6]: maximum, sum, four scales

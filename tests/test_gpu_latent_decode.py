@@ -261,7 +261,9 @@ def test_paged_bounds_and_layers(fmt):
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("R,H,longest,bound_", [(1, 8, 900, 900), (3, 8, 700, 60000), (3, 130, 900, 60000),
                                                (64, 5, 300, 3000), (64, 40, 200, 20000),
-                                               (65, 5, 300, 3000), (33, 64, 400, 401)])
+                                               (65, 5, 300, 3000), (33, 64, 400, 401),
+                                               (130, 40, 200, 9000), (512, 3, 100, 3000),
+                                               (513, 3, 100, 3000)])
 def test_paged_splits_follow_contexts(fmt, R, H, longest, bound_):
     """Ragged contexts, none at all among them, under tight and loose bounds."""
     import serving_memory_tier_amd as hs
